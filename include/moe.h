@@ -285,6 +285,121 @@ MOE_API moe_status moe_forward_fp8(const moe_config* cfg, int64_t T, const void*
                                    const moe_fp8_weights* w, void* y, float* weights_out,
                                    int32_t* idx_out, void* ws, size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------- grouped products
+ *
+ * Matrix products grouped by expert with ragged sizes, and their gradients:
+ * the single products that moe_experts_grouped fuses, for callers who train
+ * the experts or build their bodies themselves. The pages have no
+ * counterpart. Expert e owns rows [offsets[e], offsets[e+1]) of the
+ * expert-ordered matrices x [R, K] and y, dy [R, N] (act; offsets as
+ * moe_dispatch writes them) and the matrix W_e = w[e] of w [E, N, K]:
+ *
+ *   moe_grouped_matmul      y[r]  = W_e x[r]
+ *   moe_grouped_matmul_dx   dx[r] = W_e^T dy[r]
+ *   moe_grouped_matmul_dw   dw_e  = sum of dy[r] x[r]^T over e's rows
+ *
+ * Sums are in fp32 (bf16 on the tensor cores, fp32 on the CUDA cores) and
+ * rounded to the output's type once. offsets is read on the device: an expert
+ * whose pair of offsets is not 0 <= offsets[e] <= offsets[e+1] <= R sets
+ * MOE_ERR_DEVICE_CHECK in the workspace's error word and counts as one
+ * without rows (a row that two experts' ranges then share takes either's
+ * result). Experts may have no rows; rows of y and dx outside every expert's
+ * range are not written. */
+typedef struct {
+  int64_t rows;       /* R: 0 <= R < 2^31. With R == 0 the row matrices may be NULL */
+  int32_t n_experts;  /* E: 1 <= E <= 1024 */
+  int32_t n;          /* N: outputs of an expert's matrix, a multiple of 8 (bf16) / 4 (fp32) */
+  int32_t k;          /* K: its inputs, likewise; N, K <= 2^20 and N, E * K < 2^31 */
+  int32_t dtype;      /* moe_dtype */
+} moe_grouped_shape;
+
+/* Bytes of workspace the calls of this section and of the 4-bit section need
+ * for a shape (also for any shape with fewer rows); moe_workspace_init() once
+ * after allocating it. */
+MOE_API moe_status moe_grouped_workspace_size(const moe_grouped_shape* g, size_t* bytes);
+
+MOE_API moe_status moe_grouped_matmul(const moe_grouped_shape* g, const void* x,
+                                      const int32_t* offsets, const void* w, void* y, void* ws,
+                                      size_t ws_bytes, void* stream);
+
+MOE_API moe_status moe_grouped_matmul_dx(const moe_grouped_shape* g, const void* dy,
+                                         const int32_t* offsets, const void* w, void* dx, void* ws,
+                                         size_t ws_bytes, void* stream);
+
+/* dw [E, N, K] in dw_dtype (fp32 for either act, or bf16 for bf16 act). With
+ * accumulate == 0 every element of dw is written (zeros for an expert without
+ * rows); with accumulate == 1 the sum is added to dw in fp32 and rounded
+ * once, and the experts without rows keep theirs. */
+MOE_API moe_status moe_grouped_matmul_dw(const moe_grouped_shape* g, const void* dy, const void* x,
+                                         const int32_t* offsets, int32_t dw_dtype,
+                                         int32_t accumulate, void* dw, void* ws, size_t ws_bytes,
+                                         void* stream);
+
+/* ---------------------------------------------------------------- 4-bit weights
+ *
+ * Expert weights in 4 bits with one scale per group of inputs, for decoding
+ * single tokens and small batches, where the weights' bytes bound the layer.
+ * The pages have no counterpart. The layout of a matrix [N, K] (stacked per
+ * expert): codes 0..15, two to a byte along K, the lower input in the low
+ * half: q [E, N, K/2]; scales bf16 [E, K/group, N]; the weight of output i
+ * and input j is (code[i][j] - 8) * scale[j / group][i]. group is 32, 64 or
+ * 128. */
+typedef struct {
+  const void* q;       /* uint8 [E, N, K/2] */
+  const void* scales;  /* bf16 [E, K/group, N] */
+} moe_w4_matrix;
+
+/* Quantize w [E, N, K] (act; E = n_experts, rows is ignored) to that layout:
+ * each group's scale is its largest magnitude / 7 rounded to bf16 (1 for a
+ * group of zeros or one whose quotient rounds to 0), each code the nearest
+ * integer (ties to even) to w / scale, plus 8, clamped to 0..15. A group that
+ * holds a NaN or an infinity stands for NaNs. K must be a multiple of group, N of 8. */
+MOE_API moe_status moe_quantize_w4(const moe_grouped_shape* g, int32_t group, const void* w,
+                                   void* q, void* scales, void* stream);
+
+/* Products with 4-bit matrices, bf16 activations: expert e's row r reads
+ * token src[r] of x [x_rows, K], or row r itself when src is NULL (then
+ * x_rows must be R). Sums in fp32, scales applied in fp32, one rounding:
+ *
+ *   moe_grouped_matvec_w4   y[r] = W_e x[src[r]]
+ *   moe_grouped_swiglu_w4   h[r] = silu(W1_e x[src[r]]) * (W3_e x[src[r]])
+ *
+ * y, h [R, N] bf16. Any number of rows per expert is right; the form is for
+ * few (each 32 rows of an expert stream its weights again). A src outside
+ * [0, x_rows) sets MOE_ERR_DEVICE_CHECK and reads as a row of zeros; offsets
+ * are checked as above. MOE_ERR_UNSUPPORTED for fp32. */
+MOE_API moe_status moe_grouped_matvec_w4(const moe_grouped_shape* g, int32_t group, int64_t x_rows,
+                                         const void* x, const int32_t* src, const int32_t* offsets,
+                                         const moe_w4_matrix* w, void* y, void* ws,
+                                         size_t ws_bytes, void* stream);
+MOE_API moe_status moe_grouped_swiglu_w4(const moe_grouped_shape* g, int32_t group, int64_t x_rows,
+                                         const void* x, const int32_t* src, const int32_t* offsets,
+                                         const moe_w4_matrix* w1, const moe_w4_matrix* w3, void* h,
+                                         void* ws, size_t ws_bytes, void* stream);
+
+/* The experts of a layer in 4 bits (bf16 layers; dim, moe_inter and
+ * shared_inter multiples of group). */
+typedef struct {
+  moe_w4_matrix w1, w3;    /* [E, I, D] */
+  moe_w4_matrix w2;        /* [E, D, I] */
+  moe_w4_matrix ws1, ws3;  /* shared MLP [I_s, D]; NULL when shared_inter == 0 */
+  moe_w4_matrix ws2;       /* [D, I_s] */
+  int32_t group;
+} moe_w4_weights;
+
+/* Bytes of workspace moe_forward_w4 needs for T tokens. */
+MOE_API moe_status moe_workspace_size_w4(const moe_config* cfg, int64_t T, size_t* bytes);
+
+/* The whole layer with 4-bit expert weights: the router (bf16 W_r) and the
+ * dispatch as in moe_forward, the up-projections as moe_grouped_swiglu_w4
+ * (h rounded to bf16), the down-projections as moe_grouped_matvec_w4, the
+ * combine as in moe_forward. Workspace of moe_workspace_size_w4() bytes,
+ * initialised by moe_workspace_init(). */
+MOE_API moe_status moe_forward_w4(const moe_config* cfg, int64_t T, const void* x,
+                                  const void* w_router, const float* bias,
+                                  const moe_w4_weights* w, void* y, float* weights_out,
+                                  int32_t* idx_out, void* ws, size_t ws_bytes, void* stream);
+
 /* Synchronise `stream`, read and clear the workspace's error word. Returns
  * MOE_OK, MOE_ERR_DEVICE_CHECK or MOE_ERR_TIMEOUT (or MOE_ERR_CUDA). */
 MOE_API moe_status moe_check_error(void* ws, void* stream);

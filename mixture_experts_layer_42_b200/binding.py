@@ -43,7 +43,10 @@ EXPORTS = ("moe_workspace_size", "moe_workspace_init", "moe_gate", "moe_dispatch
            "moe_stage_timing_begin_every", "moe_debug_stall_pipeline",
            "moe_gate_noalloc_check_error", "moe_experts_grouped_gather", "moe_forward_ep",
            "moe_cast_output", "moe_quantize_fp8", "moe_workspace_size_fp8", "moe_forward_fp8",
-           "moe_select_fp8_kernel", "moe_fp8_kernel_for")
+           "moe_select_fp8_kernel", "moe_fp8_kernel_for", "moe_grouped_workspace_size",
+           "moe_grouped_matmul", "moe_grouped_matmul_dx", "moe_grouped_matmul_dw",
+           "moe_quantize_w4", "moe_grouped_matvec_w4", "moe_grouped_swiglu_w4",
+           "moe_workspace_size_w4", "moe_forward_w4")
 
 # Kernels of moe_forward, in launch order.
 STAGES = ("router_logits", "router_select", "dispatch_rank", "dispatch_scan", "dispatch_pos",
@@ -64,6 +67,20 @@ class moe_fp8_weights(ctypes.Structure):
                  "ws1", "ws3", "ws2", "ws1_scale", "ws3_scale", "ws2_scale")]
 
 
+class moe_grouped_shape(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("n_experts", ctypes.c_int32), ("n", ctypes.c_int32),
+                ("k", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class moe_w4_matrix(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
+class moe_w4_weights(ctypes.Structure):
+    _fields_ = [(n, moe_w4_matrix) for n in ("w1", "w3", "w2", "ws1", "ws3", "ws2")] + [
+        ("group", ctypes.c_int32)]
+
+
 class MoEError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -77,6 +94,7 @@ def _load() -> ctypes.CDLL:
     lib = ctypes.CDLL(LIB_PATH)
     P, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     C = ctypes.POINTER(moe_config)
+    G, W4 = ctypes.POINTER(moe_grouped_shape), ctypes.POINTER(moe_w4_matrix)
     sig = {
         "moe_workspace_size": [C, I64, ctypes.POINTER(SZ)],
         "moe_workspace_init": [P, SZ, P],
@@ -103,6 +121,15 @@ def _load() -> ctypes.CDLL:
         "moe_quantize_fp8": [C, P, I64, I64, I32, P, P, P],
         "moe_workspace_size_fp8": [C, I64, ctypes.POINTER(SZ)],
         "moe_forward_fp8": [C, I64, P, P, P, ctypes.POINTER(moe_fp8_weights), P, P, P, P, SZ, P],
+        "moe_grouped_workspace_size": [G, ctypes.POINTER(SZ)],
+        "moe_grouped_matmul": [G, P, P, P, P, P, SZ, P],
+        "moe_grouped_matmul_dx": [G, P, P, P, P, P, SZ, P],
+        "moe_grouped_matmul_dw": [G, P, P, P, I32, I32, P, P, SZ, P],
+        "moe_quantize_w4": [G, I32, P, P, P, P],
+        "moe_grouped_matvec_w4": [G, I32, I64, P, P, P, W4, P, P, SZ, P],
+        "moe_grouped_swiglu_w4": [G, I32, I64, P, P, P, W4, W4, P, P, SZ, P],
+        "moe_workspace_size_w4": [C, I64, ctypes.POINTER(SZ)],
+        "moe_forward_w4": [C, I64, P, P, P, ctypes.POINTER(moe_w4_weights), P, P, P, P, SZ, P],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
@@ -264,6 +291,163 @@ def moe_forward_fp8(cfg, x, w_router, bias, fw: moe_fp8_weights, y, ws, weights_
     _check(_lib.moe_forward_fp8(_c(cfg), x.shape[0], _p(x), _p(w_router), _p(bias), ctypes.byref(fw),
                                 _p(y), _p(weights_out), _p(idx_out), _p(ws), ws.numel(), _s(stream)),
            "moe_forward_fp8")
+
+
+def _need(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _s_of(stream, t: torch.Tensor) -> ctypes.c_void_p:
+    """The given stream, or the current one of t's device."""
+    return _s(torch.cuda.current_stream(t.device) if stream is None and t.is_cuda else stream)
+
+
+def _dt(dtype: torch.dtype) -> int:
+    _need(dtype in (torch.float32, torch.bfloat16), f"libmoe runs float32 and bfloat16, not {dtype}")
+    return MOE_DT_F32 if dtype == torch.float32 else MOE_DT_BF16
+
+
+def grouped_shape(rows: int, n_experts: int, n: int, k: int, dtype: torch.dtype) -> moe_grouped_shape:
+    return moe_grouped_shape(rows=int(rows), n_experts=int(n_experts), n=int(n), k=int(k),
+                             dtype=_dt(dtype))
+
+
+def moe_grouped_workspace_size(rows: int, n_experts: int, n: int, k: int, dtype: torch.dtype) -> int:
+    b = ctypes.c_size_t(0)
+    _check(_lib.moe_grouped_workspace_size(ctypes.byref(grouped_shape(rows, n_experts, n, k, dtype)),
+                                           ctypes.byref(b)), "moe_grouped_workspace_size")
+    return b.value
+
+
+def alloc_workspace_grouped(rows: int, n_experts: int, n: int, k: int, dtype=torch.bfloat16,
+                            device="cuda") -> torch.Tensor:
+    """A zero-initialised workspace for the grouped products and the 4-bit
+    products of this shape (torch allocates it)."""
+    ws = torch.empty(moe_grouped_workspace_size(rows, n_experts, n, k, dtype), dtype=torch.uint8,
+                     device=device)
+    moe_workspace_init(ws, torch.cuda.current_stream(ws.device))
+    return ws
+
+
+def _grouped(rows_x, rows_y, w, offsets, extra=()):
+    """The shape of a grouped product from its row matrices x [R, K] and
+    y [R, N] (either may be None) and the stacked weights [E, N, K]."""
+    _need(w.dim() == 3, "the experts' matrices must be one [E, N, K] tensor")
+    E, n, k = w.shape
+    R = (rows_x if rows_x is not None else rows_y).shape[0]
+    for t, cols, name in ((rows_x, k, "[R, K]"), (rows_y, n, "[R, N]")):
+        _need(t is None or tuple(t.shape) == (R, cols), f"row matrix is not {name} of the weights' shape")
+    act = (rows_x if rows_x is not None else rows_y).dtype
+    _need(all(t is None or t.dtype == act for t in (rows_x, rows_y)), "row matrices of two types")
+    _need(offsets.dtype == torch.int32 and offsets.numel() == E + 1, "offsets must be int32 [E + 1]")
+    for t in (rows_x, rows_y, offsets) + tuple(extra):
+        _need(t is None or t.device == w.device, "tensors on two devices")
+    return grouped_shape(R, E, n, k, act)
+
+
+def moe_grouped_matmul(x, offsets, w, y, ws, stream=None) -> None:
+    """y[r] = w[e] x[r] for the rows r of expert e: x [R, K], w [E, N, K], y [R, N]."""
+    g = _grouped(x, y, w, offsets, (ws,))
+    _need(w.dtype == x.dtype, "weights and rows of two types")
+    _check(_lib.moe_grouped_matmul(ctypes.byref(g), _p(x), _p(offsets), _p(w), _p(y), _p(ws),
+                                   ws.numel(), _s_of(stream, ws)), "moe_grouped_matmul")
+
+
+def moe_grouped_matmul_dx(dy, offsets, w, dx, ws, stream=None) -> None:
+    """dx[r] = w[e]^T dy[r]: dy [R, N], w [E, N, K], dx [R, K]."""
+    g = _grouped(dx, dy, w, offsets, (ws,))
+    _need(w.dtype == dy.dtype, "weights and rows of two types")
+    _check(_lib.moe_grouped_matmul_dx(ctypes.byref(g), _p(dy), _p(offsets), _p(w), _p(dx), _p(ws),
+                                      ws.numel(), _s_of(stream, ws)), "moe_grouped_matmul_dx")
+
+
+def moe_grouped_matmul_dw(dy, x, offsets, dw, ws, accumulate=False, stream=None) -> None:
+    """dw[e] (+)= sum of dy[r] x[r]^T over e's rows: dy [R, N], x [R, K],
+    dw [E, N, K] in x's type or fp32."""
+    g = _grouped(x, dy, dw, offsets, (ws,))
+    _check(_lib.moe_grouped_matmul_dw(ctypes.byref(g), _p(dy), _p(x), _p(offsets), _dt(dw.dtype),
+                                      1 if accumulate else 0, _p(dw), _p(ws), ws.numel(),
+                                      _s_of(stream, ws)), "moe_grouped_matmul_dw")
+
+
+def moe_quantize_w4(w, group, q, scales, stream=None) -> None:
+    """w [E, N, K] (fp32 or bf16) -> codes q [E, N, K / 2] (uint8) and bf16
+    scales [E, K / group, N]."""
+    E, n, k = w.shape
+    _need(q.dtype == torch.uint8 and 2 * q.numel() == w.numel(), "codes must be uint8 [E, N, K / 2]")
+    _need(scales.dtype == torch.bfloat16 and scales.numel() * int(group) == w.numel(),
+          "scales must be bfloat16 [E, K / group, N]")
+    g = grouped_shape(0, E, n, k, w.dtype)
+    _check(_lib.moe_quantize_w4(ctypes.byref(g), int(group), _p(w), _p(q), _p(scales),
+                                _s_of(stream, w)), "moe_quantize_w4")
+
+
+def _w4_shape(x, src, offsets, out, mats, ws):
+    """Shape and group of a 4-bit product from its codes q [E, N, K / 2] and
+    scales [E, K / group, N]."""
+    q, s = mats[0]
+    _need(q.dim() == 3 and s.dim() == 3, "codes [E, N, K / 2] and scales [E, K / group, N] expected")
+    E, n, k = q.shape[0], q.shape[1], 2 * q.shape[2]
+    _need(s.shape[1] > 0 and k % s.shape[1] == 0, "scales do not divide the inputs into groups")
+    for qq, ss in mats:
+        _need(qq.dtype == torch.uint8 and tuple(qq.shape) == (E, n, k // 2), "codes must be uint8 [E, N, K / 2]")
+        _need(ss.dtype == torch.bfloat16 and tuple(ss.shape) == (E, s.shape[1], n),
+              "scales must be bfloat16 [E, K / group, N]")
+    R = out.shape[0]
+    _need(x.dim() == 2 and x.shape[1] == k and tuple(out.shape) == (R, n), "x [rows, K] and out [R, N] expected")
+    _need(out.dtype == x.dtype, "rows and outputs of two types")
+    _need(src is None or (src.dtype == torch.int32 and src.numel() >= R), "src must be int32 [R]")
+    _need(offsets.dtype == torch.int32 and offsets.numel() == E + 1, "offsets must be int32 [E + 1]")
+    for t in (x, src, offsets, out, ws) + tuple(t for m in mats for t in m):
+        _need(t is None or t.device == q.device, "tensors on two devices")
+    return grouped_shape(R, E, n, k, x.dtype), k // s.shape[1]
+
+
+def _w4m(q=None, scales=None) -> moe_w4_matrix:
+    return moe_w4_matrix(None if q is None else _p(q), None if scales is None else _p(scales))
+
+
+def moe_grouped_matvec_w4(x, src, offsets, q, scales, y, ws, stream=None) -> None:
+    """y[r] = W_e x[src[r]] (x[r] when src is None), W_e in 4 bits."""
+    g, group = _w4_shape(x, src, offsets, y, ((q, scales),), ws)
+    _check(_lib.moe_grouped_matvec_w4(ctypes.byref(g), group, x.shape[0], _p(x), _p(src), _p(offsets),
+                                      ctypes.byref(_w4m(q, scales)), _p(y), _p(ws), ws.numel(),
+                                      _s_of(stream, ws)), "moe_grouped_matvec_w4")
+
+
+def moe_grouped_swiglu_w4(x, src, offsets, q1, s1, q3, s3, h, ws, stream=None) -> None:
+    """h[r] = silu(W1_e x[src[r]]) * (W3_e x[src[r]]) (x[r] when src is None)."""
+    g, group = _w4_shape(x, src, offsets, h, ((q1, s1), (q3, s3)), ws)
+    _check(_lib.moe_grouped_swiglu_w4(ctypes.byref(g), group, x.shape[0], _p(x), _p(src), _p(offsets),
+                                      ctypes.byref(_w4m(q1, s1)), ctypes.byref(_w4m(q3, s3)), _p(h),
+                                      _p(ws), ws.numel(), _s_of(stream, ws)), "moe_grouped_swiglu_w4")
+
+
+def moe_workspace_size_w4(cfg, T: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_lib.moe_workspace_size_w4(_c(cfg), int(T), ctypes.byref(n)), "moe_workspace_size_w4")
+    return n.value
+
+
+def alloc_workspace_w4(cfg, T: int, device="cuda") -> torch.Tensor:
+    ws = torch.empty(moe_workspace_size_w4(cfg, T), dtype=torch.uint8, device=device)
+    moe_workspace_init(ws, torch.cuda.current_stream(ws.device))
+    return ws
+
+
+def w4_weights(group, w1, w3, w2, ws1=None, ws3=None, ws2=None) -> moe_w4_weights:
+    """The C struct of 4-bit expert weights; each matrix is a pair (codes,
+    scales) of device tensors, kept alive by the caller."""
+    return moe_w4_weights(*[_w4m(*(m or (None, None))) for m in (w1, w3, w2, ws1, ws3, ws2)],
+                          int(group))
+
+
+def moe_forward_w4(cfg, x, w_router, bias, w4: moe_w4_weights, y, ws, weights_out=None, idx_out=None,
+                   stream=None) -> None:
+    _check(_lib.moe_forward_w4(_c(cfg), x.shape[0], _p(x), _p(w_router), _p(bias), ctypes.byref(w4),
+                               _p(y), _p(weights_out), _p(idx_out), _p(ws), ws.numel(),
+                               _s_of(stream, ws)), "moe_forward_w4")
 
 
 def moe_check_error(ws, stream=None) -> int:

@@ -1,6 +1,6 @@
 // C ABI of the MoE layer library: argument checks, workspace carving and the
 // launch sequence of each entry point (declared in include/moe.h).
-#include "common.cuh"
+#include "api_common.cuh"
 
 #include <cmath>
 #include <cstring>
@@ -15,9 +15,9 @@ int g_expert_kernel = MOE_EXPERT_KERNEL_AUTO;
 // Which form runs the FP8 expert GEMMs (see moe_select_fp8_kernel).
 int g_fp8_kernel = MOE_FP8_KERNEL_AUTO;
 
-bool aligned16(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 bool is_pow2(int v) { return v > 0 && (v & (v - 1)) == 0; }
+
+}  // namespace
 
 moe_status check_config(const moe_config* c, int64_t T) {
   if (!c || T < 1) return MOE_ERR_INVALID_ARG;
@@ -40,6 +40,8 @@ moe_status check_config(const moe_config* c, int64_t T) {
   return MOE_OK;
 }
 
+namespace {
+
 moe_status check_ws(const moe_config& c, int64_t T, void* ws, size_t ws_bytes, WsLayout* L) {
   *L = ws_layout(c, T);
   if (!ws) return MOE_ERR_WORKSPACE;
@@ -48,10 +50,7 @@ moe_status check_ws(const moe_config& c, int64_t T, void* ws, size_t ws_bytes, W
   return MOE_OK;
 }
 
-template <typename T>
-T* at(void* ws, size_t off) {
-  return reinterpret_cast<T*>(reinterpret_cast<uint8_t*>(ws) + off);
-}
+}  // namespace
 
 int num_sms_current() {
   static int cached[64] = {0};
@@ -66,8 +65,6 @@ int num_sms_current() {
   }
   return cached[dev];
 }
-
-moe_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
 // Make this thread's current device the one the caller's work lives on: the
 // device of `ptr` (a device buffer of the call), else the stream's device.
@@ -93,6 +90,10 @@ moe_status bind_device(cudaStream_t s, const void* ptr) {
   if (cur != dev && cudaSetDevice(dev) != cudaSuccess) return MOE_ERR_CUDA;
   return MOE_OK;
 }
+
+bool simt_selected() { return g_expert_kernel == MOE_EXPERT_KERNEL_SIMT; }
+
+namespace {
 
 // The expert GEMMs. The routed A rows come from x_perm (an expert-contiguous
 // copy of x) or, when x_perm is null, are gathered from x through src. With
