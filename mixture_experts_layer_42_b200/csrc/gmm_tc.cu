@@ -1,0 +1,574 @@
+// Grouped products by expert on the tensor cores (bf16): moe_grouped_matmul
+// and its gradients, one persistent kernel on CTA pairs.
+//
+//   FWD  y[r]  = W_e x[r]      M = outputs of W_e, N = rows, reduced over inputs
+//   DX   dx[r] = W_e^T dy[r]   M = inputs of W_e,  N = rows, reduced over outputs
+//   DW   dW_e  = sum dy x^T    M = outputs, N = inputs, reduced over e's rows
+//
+// The features are the MMA's M side (256 over a pair, cta_group::2) and the
+// token rows its N side, whose width follows the tile's rows in steps of 32:
+// an expert's last rows cost what they are, where 128- or 256-row tiles would
+// pad them, and a decode batch's few rows need no form of their own. A tile
+// has one or two halves of up to 256 N columns, each in one of the two TMEM
+// accumulators: two halves read their weights' tile once for up to 512 rows.
+//
+// Shared-memory tiles are 128-byte-swizzled, 64 deep in the reduction.
+// K-major operands (x, dy and w in FWD; dy in DX): rows of 64 reduction
+// elements. MN-major operands (w in DX, dy and x in DW): 64 reduction rows of
+// 64 features each, 8 KB a box; the matrix descriptor's leading offset steps
+// over the boxes (64 features), its stride over 8 reduction rows.
+//
+// Per CTA, 192 threads: warp 0 the TMA producer, warp 1 of the pair's leader
+// the MMA issuer, warps 2-5 the epilogue. Rows of a tile past its expert's
+// end are other rows of the matrix (their columns are not stored); only DW,
+// which sums over rows, reads through per-expert maps that end at the
+// expert's last row. Every wait is bounded (1 s); on expiry the kernel raises
+// the error word's timeout bit, drains its copies and returns.
+#include "gmm.cuh"
+#include "tc_common.cuh"
+
+#include <cstring>
+
+namespace moe {
+
+namespace {
+
+using namespace tc;
+
+constexpr int BK = 64;                    // reduction depth of a stage (128 bytes)
+constexpr int FM = 128;                   // features per CTA; a pair holds 256
+constexpr int MAXN = 256;                 // N columns of one half
+constexpr int TILE = FM * BK * 2;         // 16 KB: an operand tile of a stage
+constexpr int NUM_THREADS = 192;
+constexpr uint32_t TMEM_COLS = 512;
+constexpr int MAX_E = 1024;
+constexpr int EPI_BYTES = 4 * 2 * 32 * 64;  // staging: per warp two blocks of 32 rows x 32 bf16
+constexpr int NBOX = 8;                   // row boxes of 16, 32, ... 128 rows
+
+template <int MODE> struct Cfg {
+  static constexpr int HALVES = MODE == GMM_DW ? 1 : 2;
+  static constexpr int STAGE_BYTES = (1 + HALVES) * TILE;
+  static constexpr int STAGES = MODE == GMM_DW ? 6 : 4;
+  static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE_BYTES + EPI_BYTES + 256 + 2 * (MAX_E + 1) * 4;
+};
+
+struct TcGmm {
+  CUtensorMap tmA;          // FWD, DX: the weights
+  CUtensorMap tmB[NBOX];    // FWD, DX: the rows, boxes of 16 (i + 1) rows
+  const CUtensorMap* maps;  // DW: [2, E] maps of dy and of x ending at each expert's last row
+  void* out;
+  const int32_t* offsets;
+  int64_t rows;
+  int E, n, k;
+  int out_f32, accumulate;
+  int stall;                // test hook: CTA 0's MMA thread lets a wait run out
+  uint32_t* err;
+};
+
+// M features (over both CTAs of the pair), N columns and reduction depth.
+struct Tile {
+  int e;
+  int f0;      // first of the pair's 256 features
+  int c0;      // first N column: row of the matrix (FWD, DX) or input (DW)
+  int cols;    // valid N columns
+  int halves;
+  int nh;      // N columns of each half (a multiple of 32; the last may hold fewer valid)
+  int depth;   // reduction elements
+  int r0;      // DW: the expert's first row
+};
+
+// FWD, DX: expert e's rows in mt tiles of `per` rows.
+struct Sched {
+  const int32_t* P;    // smem: token-tile prefix over experts [E + 1]
+  const int32_t* off;  // smem: first row of each expert [E + 1]; count in P's companion
+  const int32_t* cnt;
+  int E, nf, nc, total, cap, n, k;
+};
+
+__device__ __forceinline__ int round32(int v) { return (v + 31) & ~31; }
+__device__ __forceinline__ int tile_rows(int count, int mt) { return round32((count + mt - 1) / mt); }
+
+template <int MODE>
+__device__ __forceinline__ Tile decode(const Sched& S, int i) {
+  Tile t;
+  if (MODE == GMM_DW) {
+    const int per = S.nf * S.nc;
+    t.e = i / per;
+    const int l = i % per;
+    t.f0 = l / S.nc * (2 * FM);
+    t.c0 = l % S.nc * MAXN;
+    t.cols = min(MAXN, S.k - t.c0);
+    t.halves = 1;
+    t.nh = round32(t.cols);
+    t.depth = S.cnt[t.e];
+    t.r0 = S.off[t.e];
+  } else {
+    const int q = i / S.nf;
+    int lo = 0, hi = S.E;  // the e with P[e] <= q < P[e + 1]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (S.P[mid] <= q) lo = mid; else hi = mid;
+    }
+    t.e = lo;
+    const int mt = S.P[lo + 1] - S.P[lo];
+    const int l = i - S.nf * S.P[lo];
+    t.f0 = l / mt * (2 * FM);
+    const int c = S.cnt[lo], per = tile_rows(c, mt), m = l % mt;
+    t.c0 = S.off[lo] + m * per;
+    t.cols = min(per, c - m * per);
+    t.halves = t.cols > MAXN ? 2 : 1;
+    t.nh = t.halves == 2 ? round32((t.cols + 1) / 2) : round32(t.cols);
+    t.depth = MODE == GMM_FWD ? S.k : S.n;
+    t.r0 = 0;
+  }
+  return t;
+}
+// N columns of half h: all but a last half's missing steps of 32
+__device__ __forceinline__ int half_n(const Tile& t, int h) {
+  return h == t.halves - 1 ? round32(t.cols - h * t.nh) : t.nh;
+}
+
+// Matrix descriptor of a K-major or MN-major operand at a stage address.
+__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(8192 >> 4) << 16) |
+         ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+template <bool MN> __device__ __forceinline__ uint64_t desc_k16(uint32_t tile, int kk) {
+  return MN ? desc_mn(tile + kk * 2048) : sdesc(tile + kk * 32);
+}
+
+template <int MODE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
+    gmm_tc_kernel(const __grid_constant__ TcGmm g) {
+  using C = Cfg<MODE>;
+  constexpr bool A_MN = MODE != GMM_FWD, B_MN = MODE == GMM_DW;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* tiles = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  uint8_t* stage_out = tiles + C::STAGES * C::STAGE_BYTES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(stage_out + EPI_BYTES);
+  uint64_t* empty = full + C::STAGES;
+  uint64_t* tfull = empty + C::STAGES;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* drain = tempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* s_cap = reinterpret_cast<volatile int*>(tmem_slot + 2);
+  int32_t* cnt = reinterpret_cast<int32_t*>(stage_out + EPI_BYTES + 256);  // [E], then P [E + 1]
+  int32_t* P = cnt + MAX_E;
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t rank = cluster_rank();
+  const bool leader = rank == 0;
+  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  const int E = g.E;
+  const int NF = MODE == GMM_DX ? g.k : g.n;  // features: M extent
+  const int nf = (NF + 2 * FM - 1) / (2 * FM);
+
+  if (warp == 0) {
+    if (lane == 0) {
+      for (int s = 0; s < C::STAGES; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
+      // tempty: one arrive per epilogue warp of both CTAs (used on the leader)
+      for (int a = 0; a < 2; ++a) { mbar_init(&tfull[a], 1); mbar_init(&tempty[a], 8); }
+      mbar_init(drain, 1);
+      *abort_flag = 0;
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    const int per = (E + 31) / 32;
+    bool bad = false;
+    int maxc = 0;
+    int tl[5] = {0, 0, 0, 0, 0};  // tiles at a cap of 512, 256, 128, 64, 32 rows
+    for (int u = 0; u < per; ++u) {
+      const int e = lane * per + u;
+      if (e < E) {
+        const Span s = expert_span(g.offsets, e, g.rows);
+        bad |= s.bad;
+        cnt[e] = s.count;
+        maxc = max(maxc, s.count);
+#pragma unroll
+        for (int c = 0; c < 5; ++c) tl[c] += (int)(((int64_t)s.count + (512 >> c) - 1) >> (9 - c));
+      }
+    }
+    if (bad && blockIdx.x == 0) set_error(g.err, ERRBIT_BAD_INDEX);
+    int cap = 512;
+    if (MODE != GMM_DW) {
+      // The rows a tile may hold. Two costs decide: a tile's traffic and MMA
+      // time, about 256 + rows, and how evenly the tiles fill the pairs.
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        maxc = max(maxc, __shfl_xor_sync(0xffffffffu, maxc, o));
+#pragma unroll
+        for (int c = 0; c < 5; ++c) tl[c] += __shfl_xor_sync(0xffffffffu, tl[c], o);
+      }
+      int64_t best = INT64_MAX;
+#pragma unroll
+      for (int c = 0; c < 5; ++c) {
+        const int64_t waves = ((int64_t)tl[c] * nf + npairs - 1) / npairs;
+        const int64_t cost = waves * (256 + min(512 >> c, round32(maxc)));
+        if (cost < best) { best = cost; cap = 512 >> c; }
+      }
+      int lsum = 0;
+      for (int u = 0; u < per; ++u) {
+        const int e = lane * per + u;
+        if (e < E) lsum += (int)(((int64_t)cnt[e] + cap - 1) / cap);
+      }
+      int incl = lsum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int p = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += p;
+      }
+      int run = incl - lsum;
+      for (int u = 0; u < per; ++u) {
+        const int e = lane * per + u;
+        if (e < E) {
+          P[e] = run;
+          run += (int)(((int64_t)cnt[e] + cap - 1) / cap);
+        }
+      }
+      if (lane == 31) P[E] = incl;
+    }
+    if (lane == 0) *s_cap = cap;
+    __syncwarp();
+  } else if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(tmem_slot)),
+                 "r"(TMEM_COLS));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // barriers of both CTAs initialised before any cross-CTA use
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  Sched S;
+  S.P = P;
+  S.off = g.offsets;
+  S.cnt = cnt;
+  S.E = E;
+  S.nf = nf;
+  S.nc = (g.k + MAXN - 1) / MAXN;
+  S.cap = *s_cap;
+  S.n = g.n;
+  S.k = g.k;
+  S.total = MODE == GMM_DW ? E * nf * S.nc : nf * P[E];
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- TMA producer (both CTAs)
+    if (lane == 0) {
+      int s = 0, issued = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int i = pair; ok && i < S.total; i += npairs) {
+        const Tile t = decode<MODE>(S, i);
+        const int kb_n = (t.depth + BK - 1) / BK;
+        if (kb_n == 0) continue;
+        const int f = t.f0 + (int)rank * FM;
+        // this CTA's N columns of each half: [c0 + h nh + rank n/2, + n/2)
+        const int n0 = half_n(t, 0), n1 = t.halves == 2 ? half_n(t, 1) : 0;
+        const int cb0 = t.c0 + (int)rank * (n0 / 2), cb1 = t.c0 + t.nh + (int)rank * (n1 / 2);
+        const CUtensorMap *ma = &g.tmA, *mb0 = nullptr, *mb1 = nullptr;
+        uint32_t tx = 2u * TILE;
+        if (MODE == GMM_DW) {
+          ma = g.maps + t.e;
+          mb0 = g.maps + E + t.e;
+          tmap_acquire(ma);
+          tmap_acquire(mb0);
+          tx += 2u * TILE;
+        } else {
+          mb0 = &g.tmB[n0 / 32 - 1];
+          if (t.halves == 2) mb1 = &g.tmB[n1 / 32 - 1];
+          tx += (uint32_t)(n0 + n1) * (BK * 2);
+        }
+        for (int kb = 0; kb < kb_n; ++kb) {
+          if (!mbar_wait(&empty[s], ph ^ 1, abort_flag, g.err)) { ok = false; break; }
+          uint8_t* sa = tiles + s * C::STAGE_BYTES;
+          uint8_t* sb = sa + TILE;
+          const uint32_t fb = mapa(smem_u32(&full[s]), 0);
+          if (leader) mbar_expect_tx(&full[s], tx);
+          const int kk = kb * BK;
+          if (MODE == GMM_FWD) {
+            tma2_load_3d(sa, ma, fb, kk, f, t.e);
+          } else if (MODE == GMM_DX) {
+            tma2_load_3d(sa, ma, fb, f, kk, t.e);
+            tma2_load_3d(sa + TILE / 2, ma, fb, f + 64, kk, t.e);
+          } else {
+            tma2_load_2d(sa, ma, fb, f, t.r0 + kk);
+            tma2_load_2d(sa + TILE / 2, ma, fb, f + 64, t.r0 + kk);
+          }
+          if (MODE == GMM_DW) {
+            const int c = t.c0 + (int)rank * (t.nh / 2);
+            tma2_load_2d(sb, mb0, fb, c, t.r0 + kk);
+            tma2_load_2d(sb + TILE / 2, mb0, fb, c + 64, t.r0 + kk);
+          } else {
+            tma2_load_2d(sb, mb0, fb, kk, cb0);
+            if (mb1) tma2_load_2d(sb + TILE, mb1, fb, kk, cb1);
+          }
+          ++issued;
+          if (++s == C::STAGES) { s = 0; ph ^= 1; }
+        }
+      }
+      if (!ok && leader)
+        for (int j = 0; j < C::STAGES; ++j) {
+          const int n = issued / C::STAGES + (j < issued % C::STAGES ? 1 : 0);
+          if (n > 0) mbar_drain(&full[j], (uint32_t)((n - 1) & 1));
+        }
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA issuer (leader)
+    if (leader && lane == 0) {
+      int s = 0;
+      uint32_t ph = 0, hb = 0;  // hb: halves so far; half i uses accumulator i & 1
+      bool ok = true;
+      if (g.stall && blockIdx.x == 0 && !mbar_wait(drain, 0, abort_flag, g.err)) ok = false;
+      for (int i = pair; ok && i < S.total; i += npairs) {
+        const Tile t = decode<MODE>(S, i);
+        const int kb_n = (t.depth + BK - 1) / BK;
+        if (kb_n == 0) continue;
+        constexpr uint32_t MAJ = (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
+        const uint32_t id0 = idesc_bf16(2 * FM, half_n(t, 0)) | MAJ;
+        const uint32_t id1 = t.halves == 2 ? idesc_bf16(2 * FM, half_n(t, 1)) | MAJ : 0u;
+        uint32_t d[2];
+        for (int h = 0; ok && h < t.halves; ++h) {
+          const uint32_t u = hb + h;
+          ok = mbar_wait(&tempty[u & 1], ((u >> 1) & 1) ^ 1, abort_flag, g.err);
+          d[h] = tmem_base + (u & 1) * MAXN;
+        }
+        if (!ok) break;
+        tc_fence_after();
+        for (int kb = 0; kb < kb_n; ++kb) {
+          if (!mbar_wait(&full[s], ph, abort_flag, g.err)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t a0 = smem_u32(tiles + s * C::STAGE_BYTES);
+          const uint32_t b0 = a0 + TILE;
+#pragma unroll
+          for (int kk = 0; kk < BK / 16; ++kk) {
+            const uint64_t ad = desc_k16<A_MN>(a0, kk);
+            mma_pair(d[0], ad, desc_k16<B_MN>(b0, kk), id0, (kb | kk) != 0 ? 1u : 0u);
+            if (C::HALVES == 2 && t.halves == 2)
+              mma_pair(d[1], ad, desc_k16<B_MN>(b0 + TILE, kk), id1, (kb | kk) != 0 ? 1u : 0u);
+          }
+          commit_pair(&empty[s]);
+          if (++s == C::STAGES) { s = 0; ph ^= 1; }
+        }
+        if (!ok) break;
+        for (int h = 0; h < t.halves; ++h) commit_pair(&tfull[(hb + h) & 1]);
+        hb += t.halves;
+      }
+      commit_pair(drain);
+      mbar_drain(drain, 0);
+    }
+  } else {
+    // ---------------------------------------------------------------- epilogue (both CTAs)
+    const int quad = warp & 3;
+    const uint32_t free_bar[2] = {mapa(smem_u32(&tempty[0]), 0), mapa(smem_u32(&tempty[1]), 0)};
+    __nv_bfloat16* stg = reinterpret_cast<__nv_bfloat16*>(stage_out + quad * (EPI_BYTES / 4));
+    uint32_t hb = 0;
+    int ok = 1;
+    for (int i = pair; ok && i < S.total; i += npairs) {
+      const Tile t = decode<MODE>(S, i);
+      const int fw = t.f0 + (int)rank * FM + quad * 32;  // this warp's first feature
+      if (t.depth == 0) {
+        // DW of an expert without rows: zeros, or nothing to add
+        if (MODE == GMM_DW && !g.accumulate && fw + lane < NF) {
+          const int64_t o = ((int64_t)t.e * g.n + fw + lane) * g.k + t.c0;
+          for (int c = 0; c < t.cols; c += 8) {
+            if (g.out_f32) {
+              float* p = static_cast<float*>(g.out) + o + c;
+              *reinterpret_cast<uint4*>(p) = make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4*>(p + 4) = make_uint4(0, 0, 0, 0);
+            } else {
+              *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(g.out) + o + c) = make_uint4(0, 0, 0, 0);
+            }
+          }
+        }
+        continue;
+      }
+      for (int h = 0; h < t.halves; ++h, ++hb) {
+        if (lane == 0) ok = mbar_wait(&tfull[hb & 1], (hb >> 1) & 1, abort_flag, g.err) ? 1 : 0;
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t tb = tmem_base + ((uint32_t)(quad * 32) << 16) + (hb & 1) * MAXN;
+        const int nv = min(t.cols - h * t.nh, t.nh);  // valid columns of this half
+        const int cb = t.c0 + h * t.nh;
+#pragma unroll 1
+        for (int c = 0; c < nv; c += 32) {
+          uint32_t ra[16], rb[16];
+          tmem_ld16(tb + c, ra);
+          tmem_ld16(tb + c + 16, rb);
+          tmem_wait_ld();
+          if (MODE == GMM_DW) {
+            // lane = output row of dw, 32 inputs
+            if (fw + lane < NF) {
+              const int64_t o = ((int64_t)t.e * g.n + fw + lane) * g.k + cb + c;
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                if (c + q * 8 >= nv) break;  // k is a multiple of 8
+                const uint32_t* r = q < 2 ? ra + q * 8 : rb + (q - 2) * 8;
+                float v[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(r[j]);
+                if (g.out_f32) {
+                  float* p = static_cast<float*>(g.out) + o + q * 8;
+                  Vec16<float> a, b;
+                  if (g.accumulate) {
+                    float old[8];
+                    a.raw = *reinterpret_cast<const uint4*>(p);
+                    b.raw = *reinterpret_cast<const uint4*>(p + 4);
+                    a.to_float(old);
+                    b.to_float(old + 4);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] += old[j];
+                  }
+                  a.from_float(v);
+                  b.from_float(v + 4);
+                  *reinterpret_cast<uint4*>(p) = a.raw;
+                  *reinterpret_cast<uint4*>(p + 4) = b.raw;
+                } else {
+                  __nv_bfloat16* p = static_cast<__nv_bfloat16*>(g.out) + o + q * 8;
+                  Vec16<__nv_bfloat16> a;
+                  if (g.accumulate) {
+                    float old[8];
+                    a.raw = *reinterpret_cast<const uint4*>(p);
+                    a.to_float(old);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] += old[j];
+                  }
+                  a.from_float(v);
+                  *reinterpret_cast<uint4*>(p) = a.raw;
+                }
+              }
+            }
+          } else {
+            // lane = feature, 32 rows: through shared memory to 64-byte
+            // pieces of the rows
+            __nv_bfloat16* blk = stg + ((c >> 5) & 1) * (32 * 32);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              blk[j * 32 + lane] = __float2bfloat16_rn(__uint_as_float(ra[j]));
+              blk[(16 + j) * 32 + lane] = __float2bfloat16_rn(__uint_as_float(rb[j]));
+            }
+            __syncwarp();
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(g.out);
+            const int fp = fw + (lane & 3) * 8;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int r = j * 8 + (lane >> 2);
+              if (c + r < nv && fp < NF)
+                *reinterpret_cast<uint4*>(out + (int64_t)(cb + c + r) * NF + fp) =
+                    *reinterpret_cast<const uint4*>(blk + r * 32 + (lane & 3) * 8);
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(free_bar[hb & 1]);
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // no remote arrive or MMA into this CTA is still pending
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
+                 "r"(TMEM_COLS));
+  }
+}
+
+// DW: each expert's copies of the maps of dy and x, ending at its last row,
+// so that a stage that reaches past it reads zeros: one warp a map.
+struct EndMapArgs {
+  CUtensorMap base[2];
+  CUtensorMap* maps;
+};
+
+__global__ void __launch_bounds__(256) gmm_end_maps_kernel(const __grid_constant__ EndMapArgs a,
+                                                           const int32_t* offsets, int64_t rows, int E) {
+  __shared__ __align__(128) CUtensorMap sm[8];
+  const int w = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int e = blockIdx.x * 8 + w;
+  if (e >= E) return;  // whole warps
+  reinterpret_cast<uint32_t*>(&sm[w])[lane] =
+      reinterpret_cast<const uint32_t*>(&a.base[blockIdx.y])[lane];
+  __syncwarp();
+  if (lane == 0) {
+    const Span s = expert_span(offsets, e, rows);
+    const int end = s.b + s.count;
+    asm volatile("tensormap.replace.tile.global_dim.shared::cta.b1024.b32 [%0], 1, %1;" ::"r"(
+                     smem_u32(&sm[w])),
+                 "r"(end > 0 ? end : 1)
+                 : "memory");
+  }
+  __syncwarp();
+  asm volatile(
+      "tensormap.cp_fenceproxy.global.shared::cta.tensormap::generic.release.gpu.sync.aligned [%0], "
+      "[%1], 128;" ::"l"(a.maps + (int64_t)blockIdx.y * E + e),
+      "r"(smem_u32(&sm[w]))
+      : "memory");
+}
+
+// bf16 maps with 128-byte swizzle: a row matrix [rows, cols] in boxes of 64
+// columns x box rows, and stacked matrices [E, n, k] in boxes of 64 inputs x
+// box outputs.
+bool map_rows(CUtensorMap* m, const void* p, int64_t rows, int cols, uint32_t box) {
+  return tc::map_2d(m, p, (uint64_t)rows, (uint64_t)cols, box);
+}
+
+template <int MODE>
+cudaError_t launch(const GmmArgs& a, void* maps, int num_sms, cudaStream_t st) {
+  using C = Cfg<MODE>;
+  TcGmm g;
+  memset(&g, 0, sizeof(g));
+  if (MODE == GMM_DW) {
+    if (a.rows > 0) {
+      EndMapArgs m;
+      m.maps = static_cast<CUtensorMap*>(maps);
+      if (!map_rows(&m.base[0], a.a, a.rows, a.n, BK) || !map_rows(&m.base[1], a.b, a.rows, a.k, BK))
+        return cudaErrorInvalidValue;
+      gmm_end_maps_kernel<<<dim3((unsigned)ceil_div(a.E, 8), 2), 256, 0, st>>>(m, a.offsets, a.rows, a.E);
+      const cudaError_t e = cudaGetLastError();
+      if (e != cudaSuccess) return e;
+    }
+    g.maps = static_cast<const CUtensorMap*>(maps);
+  } else {
+    if (a.rows == 0) return cudaSuccess;
+    if (!tc::map_3d(&g.tmA, a.b, (uint64_t)a.E, (uint64_t)a.n, (uint64_t)a.k, MODE == GMM_FWD ? FM : BK))
+      return cudaErrorInvalidValue;
+    for (int i = 0; i < NBOX; ++i)
+      if (!map_rows(&g.tmB[i], a.a, a.rows, MODE == GMM_FWD ? a.k : a.n, 16 * (i + 1)))
+        return cudaErrorInvalidValue;
+  }
+  g.out = a.out;
+  g.offsets = a.offsets;
+  g.rows = a.rows;
+  g.E = a.E;
+  g.n = a.n;
+  g.k = a.k;
+  g.out_f32 = a.out_f32;
+  g.accumulate = a.accumulate;
+  g.stall = pipeline_stall() == STALL_EXPERTS_UP ? 1 : 0;
+  g.err = a.err;
+  // upper bound on the tiles (the count depends on the device's offsets)
+  const int64_t nf = ceil_div(MODE == GMM_DX ? a.k : a.n, 2 * FM);
+  const int64_t bound = MODE == GMM_DW ? nf * ceil_div(a.k, MAXN) * a.E : nf * (a.rows / 32 + a.E);
+  const int pairs = (int)(bound < num_sms / 2 ? bound : num_sms / 2);
+  cudaError_t e = cudaFuncSetAttribute(gmm_tc_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)C::SMEM);
+  if (e != cudaSuccess) return e;
+  gmm_tc_kernel<MODE><<<2 * pairs, NUM_THREADS, C::SMEM, st>>>(g);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_gmm_tc(int mode, const GmmArgs& g, void* maps, int num_sms, cudaStream_t st) {
+  if (mode == GMM_FWD) return launch<GMM_FWD>(g, maps, num_sms, st);
+  if (mode == GMM_DX) return launch<GMM_DX>(g, maps, num_sms, st);
+  return launch<GMM_DW>(g, maps, num_sms, st);
+}
+
+}  // namespace moe

@@ -67,7 +67,11 @@ moe_status run_gmm(int mode, const moe_grouped_shape* g, const void* a, const in
   p.out_f32 = out_f32;
   p.accumulate = accumulate;
   p.err = at<uint32_t>(ws, 0);
-  return cuda_status(launch_gmm_simt(mode, g->dtype == MOE_DT_BF16, p, s));
+  const bool bf16 = g->dtype == MOE_DT_BF16;
+  if (bf16 && !simt_selected())
+    return cuda_status(launch_gmm_tc(mode, p, at<void>(ws, grouped_layout(g->n_experts).maps),
+                                     num_sms_current(), s));
+  return cuda_status(launch_gmm_simt(mode, bf16, p, s));
 }
 
 bool w4_group_ok(int group) { return group == 32 || group == 64 || group == 128; }
