@@ -358,8 +358,8 @@ MOE_API moe_status moe_quantize_w4(const moe_grouped_shape* g, int32_t group, co
                                    void* q, void* scales, void* stream);
 
 /* Products with 4-bit matrices, bf16 activations: expert e's row r reads
- * token src[r] of x [x_rows, K], or row r itself when src is NULL (then
- * x_rows must be R). Sums in fp32, scales applied in fp32, one rounding:
+ * token src[r] of x [x_rows, K] (x_rows >= 1 unless R == 0), or row r itself
+ * when src is NULL (then x_rows must be R). Sums in fp32, scales applied in fp32, one rounding:
  *
  *   moe_grouped_matvec_w4   y[r] = W_e x[src[r]]
  *   moe_grouped_swiglu_w4   h[r] = silu(W1_e x[src[r]]) * (W3_e x[src[r]])

@@ -102,7 +102,8 @@ moe_status run_w4(const moe_grouped_shape* g, int group, int64_t x_rows, const v
   if (g->dtype != MOE_DT_BF16) return MOE_ERR_UNSUPPORTED;
   if ((st = check_w4(g, group)) != MOE_OK) return st;
   if (!w1 || !matrix_ok(*w1) || (swiglu && (!w3 || !matrix_ok(*w3)))) return MOE_ERR_INVALID_ARG;
-  if (x_rows < 0 || (src == nullptr && x_rows != g->rows)) return MOE_ERR_INVALID_ARG;
+  if (x_rows < 0 || (src == nullptr && x_rows != g->rows) || (x_rows == 0 && g->rows > 0))
+    return MOE_ERR_INVALID_ARG;
   if (x_rows > (int64_t)INT32_MAX) return MOE_ERR_UNSUPPORTED;
   if (!rows_ok(x, x_rows) || !rows_ok(out, g->rows) || !aligned16(offsets)) return MOE_ERR_INVALID_ARG;
   if (src && !aligned16(src)) return MOE_ERR_INVALID_ARG;
@@ -122,7 +123,7 @@ moe_status run_w4(const moe_grouped_shape* g, int group, int64_t x_rows, const v
   p.E = g->n_experts;
   p.group = group;
   p.err = at<uint32_t>(ws, 0);
-  return cuda_status(launch_w4(swiglu, p, s));
+  return cuda_status(launch_w4(swiglu, p, num_sms_current(), s));
 }
 
 moe_status check_w4_layer(const moe_config* cfg, int64_t T, int group) {
@@ -274,7 +275,7 @@ moe_status moe_forward_w4(const moe_config* cfg, int64_t T, const void* x, const
   p.group = w->group;
   p.t_shared = sh ? T : 0;
   p.err = err;
-  if (launch_w4(true, p, s) != cudaSuccess) return MOE_ERR_CUDA;
+  if (launch_w4(true, p, num_sms_current(), s) != cudaSuccess) return MOE_ERR_CUDA;
   // down: from h in the expert order into y_perm, from the shared h into s
   void* sbuf = sh ? at<void>(ws, L.s) : nullptr;
   p.x[0] = at<__nv_bfloat16>(ws, L.h);
@@ -288,7 +289,7 @@ moe_status moe_forward_w4(const moe_config* cfg, int64_t T, const void* x, const
   p.n[0] = p.n[1] = c.dim;
   p.k[0] = c.moe_inter;
   p.k[1] = c.shared_inter;
-  if (launch_w4(false, p, s) != cudaSuccess) return MOE_ERR_CUDA;
+  if (launch_w4(false, p, num_sms_current(), s) != cudaSuccess) return MOE_ERR_CUDA;
   return cuda_status(launch_combine(c, T, at<void>(ws, L.y_perm), pos, weights, sbuf, y, s));
 }
 

@@ -25,7 +25,7 @@ struct W4Args {
   uint32_t* err;
 };
 
-cudaError_t launch_w4(bool swiglu, const W4Args& g, cudaStream_t st);
+cudaError_t launch_w4(bool swiglu, const W4Args& g, int num_sms, cudaStream_t st);
 cudaError_t launch_quantize_w4(bool bf16, const void* w, int64_t E, int n, int k, int group,
                                uint8_t* q, __nv_bfloat16* scales, cudaStream_t st);
 
