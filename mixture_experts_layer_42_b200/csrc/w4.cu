@@ -69,17 +69,18 @@ __global__ void __launch_bounds__(256) quantize_w4_kernel(const T* w, int64_t ro
 // ---------------------------------------------------------------- products
 //
 // A CTA takes a tile of 128 weight rows (SWIGLU: 64 rows of w1 over the same
-// 64 of w3) and up to 16 of their expert's token rows. A producer warp keeps
+// 64 of w3) and up to TOK of their expert's token rows. A producer warp keeps
 // STAGES stages of 256 inputs in flight: the codes by TMA (128 bytes a row,
 // 128-byte swizzle), their scales by TMA, the token rows by TMA gathers of
-// four rows. Eight warps multiply: warp (mi, ki) takes 64 weight rows and 64
-// of the stage's inputs, turns codes into bf16 in registers and feeds them to
-// mma.sync m16n8k16 as its A side, the token rows as its B side, and sums the
-// four ki at the end of the tile. The weights' bytes bound these calls, and
-// the tensor work of a few columns is far below either tensor path's rate, so
-// what decides is the way from bytes to operands: registers here, where a
-// tcgen05 operand would take the widened weights through shared or tensor
-// memory first.
+// four rows. Each of four warps multiplies 32 of the weight rows over all
+// inputs: it turns codes into bf16 in registers and feeds them to mma.sync
+// m16n8k16 as its A side, the token rows as its B side. The weights' bytes
+// bound these calls, and the tensor work of a few columns is far below either
+// tensor path's rate, so what decides is the way from bytes to operands:
+// registers here, where a tcgen05 operand would take the widened weights
+// through shared or tensor memory first. Warps own whole rows, so a tile ends
+// without a sum over warps or a barrier; in a SWIGLU tile the MMA's rows g and
+// g + 8 are the same feature of w1 and of w3, and a thread holds both sums.
 //
 // The k order within 32 inputs (16 bytes of codes) is the codes' own: quad
 // lane t holds the word of inputs 8t..8t+7; (word >> 4s) & 0x000f000f are the
@@ -91,16 +92,20 @@ using namespace tc;
 
 constexpr int KS = 256;                  // inputs per stage
 constexpr int WR = 128;                  // weight rows per tile
-constexpr int TOK = 16;                  // token rows per tile
 constexpr int W_BYTES = WR * KS / 2;     // 16 KB of codes
-constexpr int X_BYTES = TOK * KS * 2;    // 8 KB of token rows: 4 slices of [16][64]
-constexpr int S_BYTES = WR * (KS / 32) * 2;  // 2 KB of scales (group 32)
-constexpr int STAGE_BYTES = W_BYTES + X_BYTES + S_BYTES;
-constexpr int STAGES = 3;
-constexpr int RED_BYTES = 8 * 64 * 8 * 4;    // [warp][64 rows][8 tokens] fp32
-constexpr int NUM_THREADS = 288;
+constexpr int NUM_THREADS = 160;
 constexpr int MAX_E = 1024;
-constexpr size_t SMEM_BYTES = 1024 + (size_t)STAGES * STAGE_BYTES + RED_BYTES + 128 + (MAX_E + 1) * 4;
+
+// TOK = 8 NT token rows a tile; a stage's scales are [KS / group][128] bf16.
+template <int NT, bool G32> struct W4Cfg {
+  static constexpr int TOK = 8 * NT;
+  static constexpr int X_BYTES = TOK * KS * 2;  // 4 slices of [TOK][64]
+  static constexpr int S_BYTES = WR * (KS / (G32 ? 32 : 64)) * 2;
+  static constexpr int STAGE_BYTES = W_BYTES + X_BYTES + S_BYTES;
+  static constexpr int CTAS = NT == 1 ? 3 : 2;  // per SM
+  static constexpr int STAGES = NT == 2 ? 4 : 3;
+  static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE_BYTES + 256 + (MAX_E + 1) * 4;
+};
 
 struct W4Tma {
   CUtensorMap q1[2], q3[2];  // codes {k / 2, n, E}
@@ -108,59 +113,11 @@ struct W4Tma {
   CUtensorMap x[2];          // token rows, gathered
 };
 
+// What the multiplying warps need to know of a tile; rows < 0: no more tiles.
 struct W4Tile {
-  int kind, e, f0;
   int64_t row0;  // first row of the expert order (kind 0) or of x (kind 1)
-  int rows;
+  int kind, e, f0, rows;
 };
-
-struct W4Sched {
-  const int32_t* P;  // smem: token-tile prefix over experts
-  int E, nt0, nt1, mt_sh, routed, total;
-  int fw;            // features per tile
-};
-
-__device__ __forceinline__ W4Tile decode(const W4Sched& S, const W4Args& g, int i) {
-  W4Tile t;
-  if (i < S.routed) {
-    const int q = i / S.nt0;
-    int lo = 0, hi = S.E;  // the e with P[e] <= q < P[e + 1]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (S.P[mid] <= q) lo = mid; else hi = mid;
-    }
-    const int mt = S.P[lo + 1] - S.P[lo];
-    const int l = i - S.nt0 * S.P[lo];
-    const Span sp = expert_span(g.offsets, lo, g.rows);
-    t.kind = 0;
-    t.e = lo;
-    t.f0 = l / mt * S.fw;
-    t.row0 = (int64_t)sp.b + (l % mt) * TOK;
-    t.rows = min(TOK, sp.count - (l % mt) * TOK);
-  } else {
-    const int l = i - S.routed;
-    t.kind = 1;
-    t.e = 0;
-    t.f0 = l / S.mt_sh * S.fw;
-    t.row0 = (int64_t)(l % S.mt_sh) * TOK;
-    t.rows = (int)min((int64_t)TOK, g.t_shared - t.row0);
-  }
-  return t;
-}
-
-// Named barrier 1 over the eight multiplying warps that ORs a flag across them.
-__device__ __forceinline__ bool sync_any(bool flag) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, 1, 256, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"((uint32_t)flag)
-      : "memory");
-  return r != 0;
-}
 
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   uint32_t v;
@@ -187,85 +144,103 @@ template <int s> __device__ __forceinline__ uint32_t pair_of(uint32_t q) {
   return *reinterpret_cast<const uint32_t*>(&d);
 }
 
-__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// the same with a zero accumulator
+__device__ __forceinline__ void mma16816_0(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-// One stage for warp (mi, ki): acc += scale * (codes - 8) x, over its 64
-// weight rows, its 64 inputs and NT blocks of 8 tokens.
-template <int NT, bool G32>
-__device__ __forceinline__ void stage_mma(float (&acc)[4][TOK / 8][4], uint32_t wrow, uint32_t xs,
-                                          uint32_t sc, uint32_t sc_step, int ki, int gr, int t) {
+// One stage of a warp: acc += scale * (codes - 8) x over its two blocks of 16
+// weight rows, 256 inputs and NT blocks of 8 tokens. wrow: this lane's first
+// row; second block +wblk, rows 8..15 of a block +w8 (bytes; scales half of
+// an element each: sc, sblk, s8). GPC: chunks of 32 inputs per scale.
+template <int NT, int TOK, int GPC>
+__device__ __forceinline__ void stage_mma(float (&acc)[2][TOK / 8][4], uint32_t wrow, uint32_t wblk,
+                                          uint32_t w8, uint32_t x, uint32_t sc, uint32_t sblk,
+                                          uint32_t s8, uint32_t sgrp, int gr, int t) {
   const int tok = (gr >> 1) | ((gr & 1) << 2);  // token of column gr: conflict-free reads
-  uint32_t b[NT][2][4];
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
+  for (int c0 = 0; c0 < 8; c0 += GPC) {  // one group of inputs
+    float p[2][NT][4];
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const uint4 v = lds128(xs + (n * 8 + tok) * 128 + (((c * 4 + t) ^ tok) << 4));
-      b[n][c][0] = __byte_perm(v.x, v.z, 0x5410);
-      b[n][c][1] = __byte_perm(v.x, v.z, 0x7632);
-      b[n][c][2] = __byte_perm(v.y, v.w, 0x5410);
-      b[n][c][3] = __byte_perm(v.y, v.w, 0x7632);
-    }
-#pragma unroll
-  for (int m = 0; m < 4; ++m) {
-    float p[NT][4];
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      if (c == 0 || G32) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n) p[n][0] = p[n][1] = p[n][2] = p[n][3] = 0.f;
-      }
-      const uint32_t a = wrow + m * 16 * 128 + (((ki * 2 + c) ^ gr) << 4);
-      const uint32_t q0 = lds32(a), q1 = lds32(a + 8 * 128);
-      const uint32_t l0 = pair_of<0>(q0), l1 = pair_of<0>(q1), l2 = pair_of<1>(q0), l3 = pair_of<1>(q1);
-      const uint32_t h0 = pair_of<2>(q0), h1 = pair_of<2>(q1), h2 = pair_of<3>(q0), h3 = pair_of<3>(q1);
+    for (int c = c0; c < c0 + GPC; ++c) {
+      uint32_t b[NT][4];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        mma16816(p[n], l0, l1, l2, l3, b[n][c][0], b[n][c][1]);
-        mma16816(p[n], h0, h1, h2, h3, b[n][c][2], b[n][c][3]);
+        const uint4 v = lds128(x + (c >> 1) * (TOK * 128) + (n * 8 + tok) * 128 +
+                               ((((c & 1) * 4 + t) ^ tok) << 4));
+        b[n][0] = __byte_perm(v.x, v.z, 0x5410);
+        b[n][1] = __byte_perm(v.x, v.z, 0x7632);
+        b[n][2] = __byte_perm(v.y, v.w, 0x5410);
+        b[n][3] = __byte_perm(v.y, v.w, 0x7632);
       }
-      if (c == 1 || G32) {
-        const uint32_t sa = sc + m * 32 + (G32 ? c * sc_step : 0u);
-        const float s0 = lds_bf16(sa), s1 = lds_bf16(sa + 16);
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const uint32_t a = wrow + m * wblk + ((c ^ gr) << 4);
+        const uint32_t q0 = lds32(a), q1 = lds32(a + w8);
+        const uint32_t lo[4] = {pair_of<0>(q0), pair_of<0>(q1), pair_of<1>(q0), pair_of<1>(q1)};
+        const uint32_t hi[4] = {pair_of<2>(q0), pair_of<2>(q1), pair_of<3>(q0), pair_of<3>(q1)};
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          acc[m][n][0] = fmaf(s0, p[n][0], acc[m][n][0]);
-          acc[m][n][1] = fmaf(s0, p[n][1], acc[m][n][1]);
-          acc[m][n][2] = fmaf(s1, p[n][2], acc[m][n][2]);
-          acc[m][n][3] = fmaf(s1, p[n][3], acc[m][n][3]);
+          if (c == c0) mma16816_0(p[m][n], lo, b[n][0], b[n][1]);
+          else mma16816(p[m][n], lo, b[n][0], b[n][1]);
+          mma16816(p[m][n], hi, b[n][2], b[n][3]);
         }
+      }
+    }
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      const uint32_t sa = sc + m * sblk + c0 / GPC * sgrp;
+      const float s0 = lds_bf16(sa), s1 = lds_bf16(sa + s8);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        acc[m][n][0] = fmaf(s0, p[m][n][0], acc[m][n][0]);
+        acc[m][n][1] = fmaf(s0, p[m][n][1], acc[m][n][1]);
+        acc[m][n][2] = fmaf(s1, p[m][n][2], acc[m][n][2]);
+        acc[m][n][3] = fmaf(s1, p[m][n][3], acc[m][n][3]);
       }
     }
   }
 }
 
-template <bool SWIGLU, bool G32>
-__global__ void __launch_bounds__(NUM_THREADS, 2)
+template <bool SWIGLU, int NT, int GPC>
+__global__ void __launch_bounds__(NUM_THREADS, W4Cfg<NT, GPC == 1>::CTAS)
     w4_kernel(const __grid_constant__ W4Args g, const __grid_constant__ W4Tma m) {
+  using C = W4Cfg<NT, GPC == 1>;
+  constexpr int TOK = C::TOK, STAGES = C::STAGES;
+  constexpr int FW = SWIGLU ? WR / 2 : WR;  // features per tile
+  constexpr int NG = 8 / GPC;               // scales per row and stage
   extern __shared__ uint8_t smem_raw[];
   uint8_t* tiles = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-  float* red = reinterpret_cast<float*>(tiles + STAGES * STAGE_BYTES);
-  uint64_t* full = reinterpret_cast<uint64_t*>(tiles + STAGES * STAGE_BYTES + RED_BYTES);
+  uint64_t* full = reinterpret_cast<uint64_t*>(tiles + STAGES * C::STAGE_BYTES);
   uint64_t* empty = full + STAGES;
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(empty + STAGES);
-  int32_t* P = reinterpret_cast<int32_t*>(tiles + STAGES * STAGE_BYTES + RED_BYTES + 128);
+  W4Tile* info = reinterpret_cast<W4Tile*>(empty + STAGES);  // [STAGES]: the tile a stage begins
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(info + STAGES);
+  int32_t* P = reinterpret_cast<int32_t*>(tiles + STAGES * C::STAGE_BYTES + 256);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int E = g.E;
 
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 4); }
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  __syncthreads();
+
   if (warp == 0) {
-    if (lane == 0) {
-      for (int s = 0; s < STAGES; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 8); }
-      *abort_flag = 0;
-      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    }
+    // ---------------------------------------------------------------- TMA producer
+    // token tiles per expert and their exclusive prefix
     const int per = (E + 31) / 32;
     int lsum = 0;
     bool bad = false;
@@ -295,63 +270,83 @@ __global__ void __launch_bounds__(NUM_THREADS, 2)
       }
     }
     if (lane == 31) P[E] = incl;
-  }
-  __syncthreads();
-
-  W4Sched S;
-  S.P = P;
-  S.E = E;
-  S.fw = SWIGLU ? WR / 2 : WR;
-  S.nt0 = (g.n[0] + S.fw - 1) / S.fw;
-  S.nt1 = g.t_shared > 0 ? (g.n[1] + S.fw - 1) / S.fw : 0;
-  S.mt_sh = (int)((g.t_shared + TOK - 1) / TOK);
-  S.routed = S.nt0 * P[E];
-  S.total = S.routed + S.nt1 * S.mt_sh;
-
-  if (warp == 0) {
-    // ---------------------------------------------------------------- TMA producer
+    __syncwarp();
+    const int nt0 = (g.n[0] + FW - 1) / FW, nt1 = (g.n[1] + FW - 1) / FW;
+    const int mt_sh = (int)((g.t_shared + TOK - 1) / TOK);
+    const int routed = nt0 * P[E], total = routed + nt1 * mt_sh;
     int s = 0, issued = 0;
     uint32_t ph = 0;
     bool ok = true;
-    for (int i = blockIdx.x; ok && i < S.total; i += gridDim.x) {
-      const W4Tile t = decode(S, g, i);
-      const int ks = (g.k[t.kind] + KS - 1) / KS;
+    for (int i = blockIdx.x; ok; i += gridDim.x) {
+      W4Tile t;
+      t.rows = -1;
+      if (i < routed) {
+        const int q = i / nt0;
+        int lo = 0, hi = E;  // the e with P[e] <= q < P[e + 1]
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (P[mid] <= q) lo = mid; else hi = mid;
+        }
+        const int mt = P[lo + 1] - P[lo];
+        const int l = i - nt0 * P[lo];
+        const Span sp = expert_span(g.offsets, lo, g.rows);
+        t.kind = 0;
+        t.e = lo;
+        t.f0 = l / mt * FW;
+        t.row0 = (int64_t)sp.b + (l % mt) * TOK;
+        t.rows = min(TOK, sp.count - (l % mt) * TOK);
+      } else if (i < total) {
+        const int l = i - routed;
+        t.kind = 1;
+        t.e = 0;
+        t.f0 = l / mt_sh * FW;
+        t.row0 = (int64_t)(l % mt_sh) * TOK;
+        t.rows = (int)min((int64_t)TOK, g.t_shared - t.row0);
+      }
+      const bool end = t.rows < 0;
+      const int ks = end ? 1 : (g.k[t.kind] + KS - 1) / KS;
       const int nx = (t.rows + 3) >> 2;  // gathers of four rows per slice
-      // this lane's gather: slice lane % 4, rows 4 (lane / 4) ..; a row past
+      // this lane's gathers: slice lane % 4, rows 4 (lane / 4) ..; a row past
       // the tile or out of x takes the out-of-range row (zeros)
-      const int oob = (int)(t.kind == 0 ? g.x_rows : g.t_shared);
       int r[4];
+      if (!end) {
+        const int oob = (int)(t.kind == 0 ? g.x_rows : g.t_shared);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int v = (lane >> 2) * 4 + j;
-        r[j] = oob;
-        if (v < t.rows) {
-          r[j] = (int)(t.row0 + v);
-          if (t.kind == 0 && g.src != nullptr) {
-            r[j] = g.src[t.row0 + v];
-            if (r[j] < 0 || r[j] >= oob) {
-              r[j] = oob;
-              set_error(g.err, ERRBIT_BAD_INDEX);
+        for (int j = 0; j < 4; ++j) {
+          const int v = (lane >> 2) * 4 + j;
+          r[j] = oob;
+          if (v < t.rows) {
+            r[j] = (int)(t.row0 + v);
+            if (t.kind == 0 && g.src != nullptr) {
+              r[j] = g.src[t.row0 + v];
+              if (r[j] < 0 || r[j] >= oob) {
+                r[j] = oob;
+                set_error(g.err, ERRBIT_BAD_INDEX);
+              }
             }
           }
         }
       }
-      const uint32_t tx = W_BYTES + (uint32_t)(WR * (KS / g.group) * 2) + (uint32_t)(nx * 4 * KS * 2);
+      const uint32_t tx = W_BYTES + (uint32_t)(WR * NG * 2) + (uint32_t)(nx * 4 * KS * 2);
       for (int kb = 0; kb < ks; ++kb) {
         int w = 1;
         if (lane == 0) w = mbar_wait(&empty[s], ph ^ 1, abort_flag, g.err) ? 1 : 0;
         if (!__shfl_sync(0xffffffffu, w, 0)) { ok = false; break; }
-        uint8_t* sw = tiles + s * STAGE_BYTES;
+        uint8_t* sw = tiles + s * C::STAGE_BYTES;
         uint8_t* sx = sw + W_BYTES;
-        uint8_t* ss = sx + X_BYTES;
-        const int kg = kb * (KS / g.group);
+        uint8_t* ss = sx + C::X_BYTES;
+        if (lane == 0 && kb == 0) info[s] = t;
+        if (end) {
+          if (lane == 0) mbar_arrive(&full[s]);
+          break;
+        }
         if (lane == 0) {
           mbar_expect_tx(&full[s], tx);
           tma_load_3d(sw, &m.q1[t.kind], &full[s], kb * (KS / 2), t.f0, t.e);
-          tma_load_3d(ss, &m.s1[t.kind], &full[s], t.f0, kg, t.e);
+          tma_load_3d(ss, &m.s1[t.kind], &full[s], t.f0, kb * NG, t.e);
           if (SWIGLU) {
             tma_load_3d(sw + W_BYTES / 2, &m.q3[t.kind], &full[s], kb * (KS / 2), t.f0, t.e);
-            tma_load_3d(ss + (WR / 2) * (KS / g.group) * 2, &m.s3[t.kind], &full[s], t.f0, kg, t.e);
+            tma_load_3d(ss + FW * NG * 2, &m.s3[t.kind], &full[s], t.f0, kb * NG, t.e);
           }
         }
         __syncwarp();
@@ -361,6 +356,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 2)
         ++issued;
         if (++s == STAGES) { s = 0; ph ^= 1; }
       }
+      if (end) break;
     }
     if (!ok && lane == 0)
       for (int j = 0; j < STAGES; ++j) {
@@ -371,90 +367,71 @@ __global__ void __launch_bounds__(NUM_THREADS, 2)
   }
 
   // ------------------------------------------------------------------ multiply
-  const int cw = warp - 1, mi = cw >> 2, ki = cw & 3;
-  const int gr = lane >> 2, t4 = lane & 3;
-  const int ng = KS / g.group;
-  // byte offsets within a stage: this lane's weight row, its slice of the
-  // token rows, its scale
+  const int w = warp - 1, gr = lane >> 2, t4 = lane & 3;
+  // a lane's rows: plain 32w + 16m + g and + 8; SWIGLU feature 16w + 8m + g of
+  // w1 and, 64 rows on, of w3
+  const int row = (SWIGLU ? 16 : 32) * w + gr;
+  constexpr uint32_t WBLK = (SWIGLU ? 8 : 16) * 128, W8 = (SWIGLU ? 64 : 8) * 128;
+  constexpr uint32_t SBLK = (SWIGLU ? 8 : 16) * 2, S8 = SWIGLU ? FW * NG * 2 : 8 * 2;
   const uint32_t base = smem_u32(tiles);
-  const uint32_t o_w = (uint32_t)((mi * 64 + gr) * 128 + t4 * 4);
-  const uint32_t o_x = (uint32_t)(W_BYTES + ki * (TOK * 128));
-  const int sgrp = ki * 64 / g.group;  // group of the warp's first input
-  const uint32_t s_row = SWIGLU ? 64 * 2 : WR * 2;  // bytes per group of scales
-  const uint32_t o_s = (uint32_t)(W_BYTES + X_BYTES) + sgrp * s_row +
-                       (SWIGLU ? mi * ng * s_row : mi * 64 * 2) + gr * 2;
-  const int tid = threadIdx.x - 32;
+  const uint32_t o_w = (uint32_t)(row * 128 + t4 * 4);
+  const uint32_t o_s = (uint32_t)(W_BYTES + C::X_BYTES + row * 2);
   int s = 0;
   uint32_t ph = 0;
-  for (int i = blockIdx.x; i < S.total; i += gridDim.x) {
-    const W4Tile t = decode(S, g, i);
+  for (;;) {
+    int ok = 1;
+    if (lane == 0) ok = mbar_wait(&full[s], ph, abort_flag, g.err) ? 1 : 0;
+    if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+    const W4Tile t = info[s];
+    if (t.rows < 0) break;
     const int ks = (g.k[t.kind] + KS - 1) / KS;
-    const bool two = t.rows > 8;
-    float acc[4][TOK / 8][4];
+    float acc[2][NT][4];
 #pragma unroll
-    for (int a = 0; a < 4; ++a)
+    for (int a = 0; a < 2; ++a)
 #pragma unroll
-      for (int n = 0; n < TOK / 8; ++n)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int q = 0; q < 4; ++q) acc[a][n][q] = 0.f;
-    int ok = 1;
     for (int kb = 0; kb < ks; ++kb) {
-      if (lane == 0) ok = mbar_wait(&full[s], ph, abort_flag, g.err) ? 1 : 0;
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      if (!ok) break;
-      const uint32_t st = base + s * STAGE_BYTES;
-      if (two)
-        stage_mma<2, G32>(acc, st + o_w, st + o_x, st + o_s, s_row, ki, gr, t4);
+      if (kb > 0) {
+        if (lane == 0) ok = mbar_wait(&full[s], ph, abort_flag, g.err) ? 1 : 0;
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+      }
+      const uint32_t st = base + s * C::STAGE_BYTES;
+      if (NT == 1 || t.rows <= 8)
+        stage_mma<1, TOK, GPC>(acc, st + o_w, WBLK, W8, st + W_BYTES, st + o_s, SBLK, S8, FW * 2, gr, t4);
+      else if (NT == 2 || t.rows <= 16)
+        stage_mma<(NT < 2 ? NT : 2), TOK, GPC>(acc, st + o_w, WBLK, W8, st + W_BYTES, st + o_s, SBLK, S8,
+                                               FW * 2, gr, t4);
       else
-        stage_mma<1, G32>(acc, st + o_w, st + o_x, st + o_s, s_row, ki, gr, t4);
+        stage_mma<NT, TOK, GPC>(acc, st + o_w, WBLK, W8, st + W_BYTES, st + o_s, SBLK, S8, FW * 2, gr, t4);
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[s]);
       if (++s == STAGES) { s = 0; ph ^= 1; }
     }
-    // the four ki of each row, eight tokens at a time, in a fixed order
+    if (!ok) break;
+    // column 2t of a block is token t, column 2t + 1 token t + 4
     const int n_out = g.n[t.kind];
-    __nv_bfloat16* out = g.out[t.kind];
-    bool stop = false;
+    __nv_bfloat16* out = g.out[t.kind] + t.row0 * n_out;
 #pragma unroll
-    for (int n = 0; n < TOK / 8; ++n) {
-      if (n * 8 >= t.rows) break;
-      if (sync_any(!ok)) { stop = true; break; }
-      float* w = red + cw * (64 * 8);
+    for (int a = 0; a < 2; ++a) {
+      const int f = t.f0 + row + a * (SWIGLU ? 8 : 16);
 #pragma unroll
-      for (int a = 0; a < 4; ++a) {
-        float* q = w + (a * 16 + gr) * 8 + t4;
-        q[0] = acc[a][n][0];
-        q[4] = acc[a][n][1];
-        q[64] = acc[a][n][2];
-        q[68] = acc[a][n][3];
-      }
-      if (sync_any(!ok)) { stop = true; break; }
-      auto sum = [&](int row, int c) {  // weight row of the tile, token
-        const float* q = red + (row >> 6) * (4 * 64 * 8) + (row & 63) * 8 + c;
-        return ((q[0] + q[64 * 8]) + q[2 * 64 * 8]) + q[3 * 64 * 8];
-      };
-      if (SWIGLU) {
-        const int f = tid & 63;
-        if (t.f0 + f < n_out)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const int c = (tid >> 6) * 2 + u;
-            if (n * 8 + c < t.rows)
-              out[(t.row0 + n * 8 + c) * n_out + t.f0 + f] =
-                  __float2bfloat16_rn(silu_f(sum(f, c)) * sum(64 + f, c));
+        for (int h = 0; h < 2; ++h) {
+          const int c = n * 8 + t4 + 4 * h;
+          if (c >= t.rows) continue;
+          __nv_bfloat16* o = out + (int64_t)c * n_out + f;
+          if (SWIGLU) {
+            if (f < n_out) *o = __float2bfloat16_rn(silu_f(acc[a][n][h]) * acc[a][n][2 + h]);
+          } else {
+            if (f < n_out) *o = __float2bfloat16_rn(acc[a][n][h]);
+            if (f + 8 < n_out) o[8] = __float2bfloat16_rn(acc[a][n][2 + h]);
           }
-      } else {
-        const int f = tid & 127;
-        if (t.f0 + f < n_out)
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int c = (tid >> 7) * 4 + u;
-            if (n * 8 + c < t.rows)
-              out[(t.row0 + n * 8 + c) * n_out + t.f0 + f] = __float2bfloat16_rn(sum(f, c));
-          }
-      }
+        }
     }
-    if (stop) break;
   }
 }
 
@@ -501,13 +478,22 @@ bool map_scales(CUtensorMap* m, const void* p, int64_t E, int64_t groups, int64_
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool SWIGLU, bool G32>
-cudaError_t launch_w4_kernel(const W4Args& g, const W4Tma& m, int ctas, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(w4_kernel<SWIGLU, G32>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
+template <bool SWIGLU, int NT, int GPC>
+cudaError_t launch_w4_kernel(const W4Args& g, const W4Tma& m, int64_t bound, int num_sms, cudaStream_t st) {
+  using C = W4Cfg<NT, GPC == 1>;
+  cudaError_t e = cudaFuncSetAttribute(w4_kernel<SWIGLU, NT, GPC>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
   if (e != cudaSuccess) return e;
-  w4_kernel<SWIGLU, G32><<<ctas, NUM_THREADS, SMEM_BYTES, st>>>(g, m);
+  const int64_t most = (int64_t)C::CTAS * num_sms;
+  w4_kernel<SWIGLU, NT, GPC><<<(unsigned)(bound < most ? bound : most), NUM_THREADS, C::SMEM, st>>>(g, m);
   return cudaGetLastError();
+}
+
+template <bool SWIGLU, int NT>
+cudaError_t launch_w4_group(const W4Args& g, const W4Tma& m, int64_t bound, int num_sms, cudaStream_t st) {
+  if (g.group == 32) return launch_w4_kernel<SWIGLU, NT, 1>(g, m, bound, num_sms, st);
+  if (g.group == 64) return launch_w4_kernel<SWIGLU, NT, 2>(g, m, bound, num_sms, st);
+  return launch_w4_kernel<SWIGLU, NT, 4>(g, m, bound, num_sms, st);
 }
 
 }  // namespace
@@ -528,15 +514,22 @@ cudaError_t launch_w4(bool swiglu, const W4Args& g, int num_sms, cudaStream_t st
     if (swiglu && (!map_u8_3d(&m.q3[kind], g.q3[kind], E, n, k / 2, fw) ||
                    !map_scales(&m.s3[kind], g.s3[kind], E, k / g.group, n, fw, KS / g.group)))
       return cudaErrorInvalidValue;
-    bound += (int64_t)ceil_div(n, (int)fw) * (rows / TOK + (kind == 0 && rows > E ? E : rows));
+    bound += (int64_t)ceil_div(n, (int)fw) * (rows / 8 + (kind == 0 && rows > E ? E : rows));
   }
   if (bound == 0) return cudaSuccess;
-  const int ctas = (int)(bound < 2 * num_sms ? bound : 2 * num_sms);
-  if (swiglu)
-    return g.group == 32 ? launch_w4_kernel<true, true>(g, m, ctas, st)
-                         : launch_w4_kernel<true, false>(g, m, ctas, st);
-  return g.group == 32 ? launch_w4_kernel<false, true>(g, m, ctas, st)
-                       : launch_w4_kernel<false, false>(g, m, ctas, st);
+  // token rows per tile, by the rows an expert has on average
+  const int64_t avg = g.rows / g.E;
+  const int nt = avg <= 5 ? 1 : avg <= 12 ? 2 : 4;
+#define MOE_W4(S, N) return launch_w4_group<S, N>(g, m, bound, num_sms, st)
+  if (swiglu) {
+    if (nt == 1) MOE_W4(true, 1);
+    if (nt == 2) MOE_W4(true, 2);
+    MOE_W4(true, 4);
+  }
+  if (nt == 1) MOE_W4(false, 1);
+  if (nt == 2) MOE_W4(false, 2);
+  MOE_W4(false, 4);
+#undef MOE_W4
 }
 
 }  // namespace moe
