@@ -137,7 +137,8 @@ __device__ __forceinline__ float lds_bf16(uint32_t a) {
 
 // Codes s and s + 4 of a word as the bf16 pair of their integers code - 8.
 template <int s> __device__ __forceinline__ uint32_t pair_of(uint32_t q) {
-  uint32_t v = ((q >> (4 * s)) & 0x000f000fu) | 0x43004300u;
+  uint32_t v;  // ((q >> 4 s) & 0x000f000f) | 0x43004300 in one logic operation
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(v) : "r"(q >> (4 * s)), "r"(0x000f000fu), "r"(0x43004300u));
   const uint32_t b = 0x43084308u;  // 136, 136
   const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v),
                                    *reinterpret_cast<const __nv_bfloat162*>(&b));
