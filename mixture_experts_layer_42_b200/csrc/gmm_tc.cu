@@ -18,8 +18,14 @@
 // 64 features each, 8 KB a box; the matrix descriptor's leading offset steps
 // over the boxes (64 features), its stride over 8 reduction rows.
 //
-// Per CTA, 192 threads: warp 0 the TMA producer, warp 1 of the pair's leader
-// the MMA issuer, warps 2-5 the epilogue. Rows of a tile past its expert's
+// Stages of the shared-memory ring are as large as their tile's operands, so
+// that the same 200 KB hold 11 stages of a decode tile and 4 of a tile of 512
+// rows: what covers the memory's latency is bytes in flight.
+//
+// Per CTA, 320 threads: warp 0 the TMA producer, warp 1 of the pair's leader
+// the MMA issuer, warps 2-9 the epilogue (two warps on each 32 TMEM lanes, in
+// turn over the columns). dw leaves through shared memory by TMA stores, or
+// TMA additions to a fp32 dw that is accumulated into. Rows of a tile past its expert's
 // end are other rows of the matrix (their columns are not stored); only DW,
 // which sums over rows, reads through per-expert maps that end at the
 // expert's last row. Every wait is bounded (1 s); on expiry the kernel raises
@@ -39,22 +45,25 @@ constexpr int BK = 64;                    // reduction depth of a stage (128 byt
 constexpr int FM = 128;                   // features per CTA; a pair holds 256
 constexpr int MAXN = 256;                 // N columns of one half
 constexpr int TILE = FM * BK * 2;         // 16 KB: an operand tile of a stage
-constexpr int NUM_THREADS = 192;
+constexpr int NUM_THREADS = 320;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int MAX_E = 1024;
-constexpr int EPI_BYTES = 4 * 2 * 32 * 64;  // staging: per warp two blocks of 32 rows x 32 bf16
 constexpr int NBOX = 8;                   // row boxes of 16, 32, ... 128 rows
+constexpr int SLOTS = 12;                 // stages in flight, at most
 
 template <int MODE> struct Cfg {
   static constexpr int HALVES = MODE == GMM_DW ? 1 : 2;
-  static constexpr int STAGE_BYTES = (1 + HALVES) * TILE;
-  static constexpr int STAGES = MODE == GMM_DW ? 6 : 4;
-  static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE_BYTES + EPI_BYTES + 256 + 2 * (MAX_E + 1) * 4;
+  static constexpr int RING = MODE == GMM_DW ? 5 * 2 * TILE : 200 * 1024;
+  // staging of an epilogue warp: DW 32 rows of 128 bytes for a TMA store, else
+  // 32 rows x 32 bf16
+  static constexpr int STG = MODE == GMM_DW ? 4096 : 2048;
+  static constexpr size_t SMEM = 1024 + RING + 8 * STG + 512 + (2 * MAX_E + 1) * 4;
 };
 
 struct TcGmm {
   CUtensorMap tmA;          // FWD, DX: the weights
   CUtensorMap tmB[NBOX];    // FWD, DX: the rows, boxes of 16 (i + 1) rows
+  CUtensorMap tmO;          // DW: dw, in boxes of 128 bytes x 32 outputs
   const CUtensorMap* maps;  // DW: [2, E] maps of dy and of x ending at each expert's last row
   void* out;
   const int32_t* offsets;
@@ -137,6 +146,45 @@ template <bool MN> __device__ __forceinline__ uint64_t desc_k16(uint32_t tile, i
   return MN ? desc_mn(tile + kk * 2048) : sdesc(tile + kk * 32);
 }
 
+// Stage of a tile: A, then the halves of B; the ring's position after it.
+template <int MODE> __device__ __forceinline__ uint32_t stage_bytes(const Tile& t) {
+  if (MODE == GMM_DW) return 2 * TILE;
+  const uint32_t n = (uint32_t)(half_n(t, 0) + (t.halves == 2 ? half_n(t, 1) : 0));
+  return (TILE + n * BK + 1023) & ~1023u;
+}
+
+// Position in the ring of stages: its slot (barriers) and phase, and its byte
+// offset. The same sequence in every role of both CTAs.
+template <int MODE> struct Ring {
+  uint32_t slot = 0, ph = 0, pos = 0, pad = 0;
+  // where a stage of b bytes goes: at pos, or at the ring's start if it would
+  // straddle the end
+  __device__ __forceinline__ uint32_t place(uint32_t b) {
+    pad = 0;
+    if (pos + b > (uint32_t)Cfg<MODE>::RING) {
+      pad = Cfg<MODE>::RING - pos;
+      pos = 0;
+    }
+    return pos;
+  }
+  __device__ __forceinline__ void advance(uint32_t b) {
+    pos += b;
+    if (++slot == SLOTS) { slot = 0; ph ^= 1; }
+  }
+};
+
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* tm, const void* src, int c0, int c1, int c2) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(tm),
+               "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+}
+__device__ __forceinline__ void tma_add_3d(const CUtensorMap* tm, const void* src, int c0, int c1, int c2) {
+  asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   tm),
+               "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+}
+
 template <int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     gmm_tc_kernel(const __grid_constant__ TcGmm g) {
@@ -144,16 +192,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
   constexpr bool A_MN = MODE != GMM_FWD, B_MN = MODE == GMM_DW;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* tiles = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-  uint8_t* stage_out = tiles + C::STAGES * C::STAGE_BYTES;
-  uint64_t* full = reinterpret_cast<uint64_t*>(stage_out + EPI_BYTES);
-  uint64_t* empty = full + C::STAGES;
-  uint64_t* tfull = empty + C::STAGES;
+  uint8_t* stage_out = tiles + C::RING;
+  uint64_t* full = reinterpret_cast<uint64_t*>(stage_out + 8 * C::STG);
+  uint64_t* empty = full + SLOTS;
+  uint64_t* tfull = empty + SLOTS;
   uint64_t* tempty = tfull + 2;
   uint64_t* drain = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* s_cap = reinterpret_cast<volatile int*>(tmem_slot + 2);
-  int32_t* cnt = reinterpret_cast<int32_t*>(stage_out + EPI_BYTES + 256);  // [E], then P [E + 1]
+  uint32_t* vstart = tmem_slot + 3;  // the producer's stage starts, [SLOTS]
+  int32_t* cnt = reinterpret_cast<int32_t*>(stage_out + 8 * C::STG + 512);  // [E], then P [E + 1]
   int32_t* P = cnt + MAX_E;
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -166,9 +215,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
 
   if (warp == 0) {
     if (lane == 0) {
-      for (int s = 0; s < C::STAGES; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
+      for (int s = 0; s < SLOTS; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
       // tempty: one arrive per epilogue warp of both CTAs (used on the leader)
-      for (int a = 0; a < 2; ++a) { mbar_init(&tfull[a], 1); mbar_init(&tempty[a], 8); }
+      for (int a = 0; a < 2; ++a) { mbar_init(&tfull[a], 1); mbar_init(&tempty[a], 16); }
       mbar_init(drain, 1);
       *abort_flag = 0;
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -257,13 +306,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
   if (warp == 0) {
     // ---------------------------------------------------------------- TMA producer (both CTAs)
     if (lane == 0) {
-      int s = 0, issued = 0;
-      uint32_t ph = 0;
+      Ring<MODE> R;
+      // stages issued and known to be consumed; bytes of the ring given out,
+      // padding included (differences only: both may wrap)
+      uint32_t issued = 0, done = 0, vpos = 0, dslot = 0, dph = 0;
+      int last_e = -1;
       bool ok = true;
       for (int i = pair; ok && i < S.total; i += npairs) {
         const Tile t = decode<MODE>(S, i);
         const int kb_n = (t.depth + BK - 1) / BK;
         if (kb_n == 0) continue;
+        const uint32_t sz = stage_bytes<MODE>(t);
         const int f = t.f0 + (int)rank * FM;
         // this CTA's N columns of each half: [c0 + h nh + rank n/2, + n/2)
         const int n0 = half_n(t, 0), n1 = t.halves == 2 ? half_n(t, 1) : 0;
@@ -273,8 +326,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         if (MODE == GMM_DW) {
           ma = g.maps + t.e;
           mb0 = g.maps + E + t.e;
-          tmap_acquire(ma);
-          tmap_acquire(mb0);
+          if (t.e != last_e) {
+            tmap_acquire(ma);
+            tmap_acquire(mb0);
+            last_e = t.e;
+          }
           tx += 2u * TILE;
         } else {
           mb0 = &g.tmB[n0 / 32 - 1];
@@ -282,11 +338,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
           tx += (uint32_t)(n0 + n1) * (BK * 2);
         }
         for (int kb = 0; kb < kb_n; ++kb) {
-          if (!mbar_wait(&empty[s], ph ^ 1, abort_flag, g.err)) { ok = false; break; }
-          uint8_t* sa = tiles + s * C::STAGE_BYTES;
+          uint8_t* sa = tiles + R.place(sz);
           uint8_t* sb = sa + TILE;
-          const uint32_t fb = mapa(smem_u32(&full[s]), 0);
-          if (leader) mbar_expect_tx(&full[s], tx);
+          const uint32_t vend = vpos + R.pad + sz;
+          // the oldest stages out of the way: a slot and the bytes
+          while (issued != done && (issued - done == SLOTS || vend - vstart[dslot] > (uint32_t)C::RING)) {
+            if (!mbar_wait(&empty[dslot], dph, abort_flag, g.err)) { ok = false; break; }
+            ++done;
+            if (++dslot == SLOTS) { dslot = 0; dph ^= 1; }
+          }
+          if (!ok) break;
+          vstart[R.slot] = vpos + R.pad;
+          vpos = vend;
+          const uint32_t fb = mapa(smem_u32(&full[R.slot]), 0);
+          if (leader) mbar_expect_tx(&full[R.slot], tx);
           const int kk = kb * BK;
           if (MODE == GMM_FWD) {
             tma2_load_3d(sa, ma, fb, kk, f, t.e);
@@ -303,29 +368,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
             tma2_load_2d(sb + TILE / 2, mb0, fb, c + 64, t.r0 + kk);
           } else {
             tma2_load_2d(sb, mb0, fb, kk, cb0);
-            if (mb1) tma2_load_2d(sb + TILE, mb1, fb, kk, cb1);
+            if (mb1) tma2_load_2d(sb + n0 * BK, mb1, fb, kk, cb1);
           }
           ++issued;
-          if (++s == C::STAGES) { s = 0; ph ^= 1; }
+          R.advance(sz);
         }
       }
       if (!ok && leader)
-        for (int j = 0; j < C::STAGES; ++j) {
-          const int n = issued / C::STAGES + (j < issued % C::STAGES ? 1 : 0);
-          if (n > 0) mbar_drain(&full[j], (uint32_t)((n - 1) & 1));
+        for (uint32_t j = 0; j < SLOTS; ++j) {
+          const uint32_t n = issued / SLOTS + (j < issued % SLOTS ? 1 : 0);
+          if (n > 0) mbar_drain(&full[j], (n - 1) & 1);
         }
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer (leader)
     if (leader && lane == 0) {
-      int s = 0;
-      uint32_t ph = 0, hb = 0;  // hb: halves so far; half i uses accumulator i & 1
+      Ring<MODE> R;
+      uint32_t hb = 0;  // hb: halves so far; half i uses accumulator i & 1
       bool ok = true;
       if (g.stall && blockIdx.x == 0 && !mbar_wait(drain, 0, abort_flag, g.err)) ok = false;
       for (int i = pair; ok && i < S.total; i += npairs) {
         const Tile t = decode<MODE>(S, i);
         const int kb_n = (t.depth + BK - 1) / BK;
         if (kb_n == 0) continue;
+        const uint32_t sz = stage_bytes<MODE>(t), b1 = (uint32_t)half_n(t, 0) * BK;
         constexpr uint32_t MAJ = (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
         const uint32_t id0 = idesc_bf16(2 * FM, half_n(t, 0)) | MAJ;
         const uint32_t id1 = t.halves == 2 ? idesc_bf16(2 * FM, half_n(t, 1)) | MAJ : 0u;
@@ -338,19 +404,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         if (!ok) break;
         tc_fence_after();
         for (int kb = 0; kb < kb_n; ++kb) {
-          if (!mbar_wait(&full[s], ph, abort_flag, g.err)) { ok = false; break; }
+          const uint32_t a0 = smem_u32(tiles) + R.place(sz);
+          if (!mbar_wait(&full[R.slot], R.ph, abort_flag, g.err)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t a0 = smem_u32(tiles + s * C::STAGE_BYTES);
           const uint32_t b0 = a0 + TILE;
 #pragma unroll
           for (int kk = 0; kk < BK / 16; ++kk) {
             const uint64_t ad = desc_k16<A_MN>(a0, kk);
             mma_pair(d[0], ad, desc_k16<B_MN>(b0, kk), id0, (kb | kk) != 0 ? 1u : 0u);
             if (C::HALVES == 2 && t.halves == 2)
-              mma_pair(d[1], ad, desc_k16<B_MN>(b0 + TILE, kk), id1, (kb | kk) != 0 ? 1u : 0u);
+              mma_pair(d[1], ad, desc_k16<B_MN>(b0 + b1, kk), id1, (kb | kk) != 0 ? 1u : 0u);
           }
-          commit_pair(&empty[s]);
-          if (++s == C::STAGES) { s = 0; ph ^= 1; }
+          commit_pair(&empty[R.slot]);
+          R.advance(sz);
         }
         if (!ok) break;
         for (int h = 0; h < t.halves; ++h) commit_pair(&tfull[(hb + h) & 1]);
@@ -361,112 +427,129 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     }
   } else {
     // ---------------------------------------------------------------- epilogue (both CTAs)
-    const int quad = warp & 3;
+    const int quad = warp & 3, cg = (warp - 2) >> 2;  // TMEM lanes, turn over the columns
     const uint32_t free_bar[2] = {mapa(smem_u32(&tempty[0]), 0), mapa(smem_u32(&tempty[1]), 0)};
-    __nv_bfloat16* stg = reinterpret_cast<__nv_bfloat16*>(stage_out + quad * (EPI_BYTES / 4));
+    uint8_t* stg = stage_out + (warp - 2) * C::STG;
+    // columns a warp takes at once
+    const int step = MODE == GMM_DW && !g.out_f32 ? 64 : 32;
+    const bool direct = MODE == GMM_DW && g.accumulate && !g.out_f32;
     uint32_t hb = 0;
     int ok = 1;
     for (int i = pair; ok && i < S.total; i += npairs) {
       const Tile t = decode<MODE>(S, i);
       const int fw = t.f0 + (int)rank * FM + quad * 32;  // this warp's first feature
-      if (t.depth == 0) {
-        // DW of an expert without rows: zeros, or nothing to add
-        if (MODE == GMM_DW && !g.accumulate && fw + lane < NF) {
-          const int64_t o = ((int64_t)t.e * g.n + fw + lane) * g.k + t.c0;
-          for (int c = 0; c < t.cols; c += 8) {
-            if (g.out_f32) {
-              float* p = static_cast<float*>(g.out) + o + c;
-              *reinterpret_cast<uint4*>(p) = make_uint4(0, 0, 0, 0);
-              *reinterpret_cast<uint4*>(p + 4) = make_uint4(0, 0, 0, 0);
-            } else {
-              *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(g.out) + o + c) = make_uint4(0, 0, 0, 0);
-            }
-          }
+      const bool zero = t.depth == 0;  // DW of an expert without rows
+      if (zero && g.accumulate) continue;
+      for (int h = 0; h < t.halves; ++h) {
+        if (!zero) {
+          if (lane == 0) ok = mbar_wait(&tfull[hb & 1], (hb >> 1) & 1, abort_flag, g.err) ? 1 : 0;
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          if (!ok) break;
+          tc_fence_after();
         }
-        continue;
-      }
-      for (int h = 0; h < t.halves; ++h, ++hb) {
-        if (lane == 0) ok = mbar_wait(&tfull[hb & 1], (hb >> 1) & 1, abort_flag, g.err) ? 1 : 0;
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) break;
-        tc_fence_after();
         const uint32_t tb = tmem_base + ((uint32_t)(quad * 32) << 16) + (hb & 1) * MAXN;
         const int nv = min(t.cols - h * t.nh, t.nh);  // valid columns of this half
         const int cb = t.c0 + h * t.nh;
 #pragma unroll 1
-        for (int c = 0; c < nv; c += 32) {
-          uint32_t ra[16], rb[16];
-          tmem_ld16(tb + c, ra);
-          tmem_ld16(tb + c + 16, rb);
-          tmem_wait_ld();
-          if (MODE == GMM_DW) {
-            // lane = output row of dw, 32 inputs
-            if (fw + lane < NF) {
-              const int64_t o = ((int64_t)t.e * g.n + fw + lane) * g.k + cb + c;
+        for (int c = cg * step; c < nv; c += 2 * step) {
+          uint32_t r[32];
+          __syncwarp();
+          if (!zero) {
+            tmem_ld16(tb + c, *reinterpret_cast<uint32_t(*)[16]>(r));
+            tmem_ld16(tb + c + 16, *reinterpret_cast<uint32_t(*)[16]>(r + 16));
+            tmem_wait_ld();
+          } else {
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                if (c + q * 8 >= nv) break;  // k is a multiple of 8
-                const uint32_t* r = q < 2 ? ra + q * 8 : rb + (q - 2) * 8;
-                float v[8];
+            for (int j = 0; j < 32; ++j) r[j] = 0;
+          }
+          if (MODE == GMM_DW && !direct) {
+            // lane = output row of dw; 128 bytes of inputs through shared
+            // memory (16-byte places swizzled by row) and a TMA store
+            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            __syncwarp();
+            uint4* row = reinterpret_cast<uint4*>(stg + lane * 128);
+            if (g.out_f32) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(r[j]);
-                if (g.out_f32) {
-                  float* p = static_cast<float*>(g.out) + o + q * 8;
-                  Vec16<float> a, b;
-                  if (g.accumulate) {
-                    float old[8];
-                    a.raw = *reinterpret_cast<const uint4*>(p);
-                    b.raw = *reinterpret_cast<const uint4*>(p + 4);
-                    a.to_float(old);
-                    b.to_float(old + 4);
+              for (int j = 0; j < 8; ++j)
+                row[j ^ (lane & 7)] = make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+            } else {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) v[j] += old[j];
-                  }
-                  a.from_float(v);
-                  b.from_float(v + 4);
-                  *reinterpret_cast<uint4*>(p) = a.raw;
-                  *reinterpret_cast<uint4*>(p + 4) = b.raw;
-                } else {
-                  __nv_bfloat16* p = static_cast<__nv_bfloat16*>(g.out) + o + q * 8;
-                  Vec16<__nv_bfloat16> a;
-                  if (g.accumulate) {
-                    float old[8];
-                    a.raw = *reinterpret_cast<const uint4*>(p);
-                    a.to_float(old);
+              for (int u = 0; u < 2; ++u) {
+                if (u == 1 && !zero) {
+                  tmem_ld16(tb + c + 32, *reinterpret_cast<uint32_t(*)[16]>(r));
+                  tmem_ld16(tb + c + 48, *reinterpret_cast<uint32_t(*)[16]>(r + 16));
+                  tmem_wait_ld();
+                }
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) v[j] += old[j];
-                  }
-                  a.from_float(v);
-                  *reinterpret_cast<uint4*>(p) = a.raw;
+                for (int j = 0; j < 4; ++j) {
+                  Vec16<__nv_bfloat16> v;
+                  v.from_float(reinterpret_cast<const float*>(r) + 8 * j);
+                  row[(u * 4 + j) ^ (lane & 7)] = v.raw;
                 }
               }
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0 && fw < NF) {
+              if (g.accumulate) tma_add_3d(&g.tmO, stg, cb + c, fw, t.e);
+              else tma_store_3d(&g.tmO, stg, cb + c, fw, t.e);
+              asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            }
+          } else if (MODE == GMM_DW) {
+            // accumulation into a bf16 dw: its values in fp32, one rounding
+            // (the TMEM loads are the whole warp's, whatever its rows)
+            const int64_t o = ((int64_t)t.e * g.n + fw + lane) * g.k + cb + c;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              if (c + u * 32 >= nv) break;
+              if (u == 1) {
+                tmem_ld16(tb + c + 32, *reinterpret_cast<uint32_t(*)[16]>(r));
+                tmem_ld16(tb + c + 48, *reinterpret_cast<uint32_t(*)[16]>(r + 16));
+                tmem_wait_ld();
+              }
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                if (fw + lane >= NF || c + u * 32 + q * 8 >= nv) continue;  // k is a multiple of 8
+                __nv_bfloat16* p = static_cast<__nv_bfloat16*>(g.out) + o + u * 32 + q * 8;
+                Vec16<__nv_bfloat16> v;
+                float old[8];
+                v.raw = *reinterpret_cast<const uint4*>(p);
+                v.to_float(old);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) old[j] += __uint_as_float(r[q * 8 + j]);
+                v.from_float(old);
+                *reinterpret_cast<uint4*>(p) = v.raw;
+              }
+              __syncwarp();
             }
           } else {
             // lane = feature, 32 rows: through shared memory to 64-byte
             // pieces of the rows
-            __nv_bfloat16* blk = stg + ((c >> 5) & 1) * (32 * 32);
+            __nv_bfloat16* blk = reinterpret_cast<__nv_bfloat16*>(stg);
+            __syncwarp();
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              blk[j * 32 + lane] = __float2bfloat16_rn(__uint_as_float(ra[j]));
-              blk[(16 + j) * 32 + lane] = __float2bfloat16_rn(__uint_as_float(rb[j]));
-            }
+            for (int j = 0; j < 32; ++j) blk[j * 32 + lane] = __float2bfloat16_rn(__uint_as_float(r[j]));
             __syncwarp();
             __nv_bfloat16* out = static_cast<__nv_bfloat16*>(g.out);
             const int fp = fw + (lane & 3) * 8;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const int r = j * 8 + (lane >> 2);
-              if (c + r < nv && fp < NF)
-                *reinterpret_cast<uint4*>(out + (int64_t)(cb + c + r) * NF + fp) =
-                    *reinterpret_cast<const uint4*>(blk + r * 32 + (lane & 3) * 8);
+              const int q = j * 8 + (lane >> 2);
+              if (c + q < nv && fp < NF)
+                *reinterpret_cast<uint4*>(out + (int64_t)(cb + c + q) * NF + fp) =
+                    *reinterpret_cast<const uint4*>(blk + q * 32 + (lane & 3) * 8);
             }
           }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(free_bar[hb & 1]);
+        if (!zero) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(free_bar[hb & 1]);
+          ++hb;
+        }
       }
     }
+    if (MODE == GMM_DW && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
 
   tc_fence_before();
@@ -518,6 +601,21 @@ bool map_rows(CUtensorMap* m, const void* p, int64_t rows, int cols, uint32_t bo
   return tc::map_2d(m, p, (uint64_t)rows, (uint64_t)cols, box);
 }
 
+// dw [E, n, k] in boxes of 128 bytes x 32 outputs, for stores.
+bool map_out(CUtensorMap* m, const void* p, int E, int n, int k, bool f32) {
+  auto fn = tc::encode_fn();
+  if (!fn) return false;
+  const cuuint64_t el = f32 ? 4 : 2;
+  cuuint64_t dims[3] = {(cuuint64_t)k, (cuuint64_t)n, (cuuint64_t)E};
+  cuuint64_t strides[2] = {k * el, (cuuint64_t)n * k * el};
+  cuuint32_t box[3] = {(cuuint32_t)(128 / el), 32, 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  return fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+            const_cast<void*>(p), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int MODE>
 cudaError_t launch(const GmmArgs& a, void* maps, int num_sms, cudaStream_t st) {
   using C = Cfg<MODE>;
@@ -534,6 +632,7 @@ cudaError_t launch(const GmmArgs& a, void* maps, int num_sms, cudaStream_t st) {
       if (e != cudaSuccess) return e;
     }
     g.maps = static_cast<const CUtensorMap*>(maps);
+    if (!map_out(&g.tmO, a.out, a.E, a.n, a.k, a.out_f32)) return cudaErrorInvalidValue;
   } else {
     if (a.rows == 0) return cudaSuccess;
     if (!tc::map_3d(&g.tmA, a.b, (uint64_t)a.E, (uint64_t)a.n, (uint64_t)a.k, MODE == GMM_FWD ? FM : BK))
