@@ -48,7 +48,7 @@ constexpr int TILE = FM * BK * 2;         // 16 KB: an operand tile of a stage
 constexpr int NUM_THREADS = 320;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int MAX_E = 1024;
-constexpr int NBOX = 8;                   // row boxes of 16, 32, ... 128 rows
+constexpr int NBOX = 9;                   // row boxes of 8, 16, 32, 48, ... 128 rows
 constexpr int SLOTS = 12;                 // stages in flight, at most
 
 template <int MODE> struct Cfg {
@@ -62,7 +62,7 @@ template <int MODE> struct Cfg {
 
 struct TcGmm {
   CUtensorMap tmA;          // FWD, DX: the weights
-  CUtensorMap tmB[NBOX];    // FWD, DX: the rows, boxes of 16 (i + 1) rows
+  CUtensorMap tmB[NBOX];    // FWD, DX: the rows, boxes of 8, 16, 32, 48, ... 128 rows
   CUtensorMap tmO;          // DW: dw, in boxes of 128 bytes x 32 outputs
   const CUtensorMap* maps;  // DW: [2, E] maps of dy and of x ending at each expert's last row
   void* out;
@@ -70,6 +70,7 @@ struct TcGmm {
   int64_t rows;
   int E, n, k;
   int out_f32, accumulate;
+  int wide;                 // MN-major A by one box of 128 features (rows of whole 64s)
   int stall;                // test hook: CTA 0's MMA thread lets a wait run out
   uint32_t* err;
 };
@@ -137,14 +138,73 @@ __device__ __forceinline__ int half_n(const Tile& t, int h) {
   return h == t.halves - 1 ? round32(t.cols - h * t.nh) : t.nh;
 }
 
-// Matrix descriptor of a K-major or MN-major operand at a stage address.
-__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr) {
-  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(8192 >> 4) << 16) |
-         ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+// Matrix descriptors: the upper word is the same for both majors (128-byte
+// swizzle, 8-row groups 1024 bytes apart), the lower holds the address / 16
+// and the leading offset (MN-major: 8 KB boxes of 64 features; unused for
+// K-major). A step of 16 in the reduction is 32 bytes of a K-major tile and
+// 2048 bytes of an MN-major one.
+constexpr uint32_t DESC_HI = (1024 >> 4) | (1u << 14) | (2u << 29);
+template <bool MN> __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr) {
+  return (saddr >> 4) | (MN ? (8192u >> 4) << 16 : 1u << 16);
 }
-template <bool MN> __device__ __forceinline__ uint64_t desc_k16(uint32_t tile, int kk) {
-  return MN ? desc_mn(tile + kk * 2048) : sdesc(tile + kk * 32);
+template <bool MN> constexpr uint32_t K16 = MN ? 2048 >> 4 : 32 >> 4;
+
+__device__ __forceinline__ void mma_pair_lo(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 da, {%1, %5};\n\t"
+      "mov.b64 db, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(DESC_HI)
+      : "memory");
 }
+
+// The MMAs of a stage: a0, b0, b1 its operands' lower descriptor words.
+template <bool A_MN, bool B_MN, bool TWO>
+__device__ __forceinline__ void mma_stage(uint32_t d0, uint32_t d1, uint32_t a0, uint32_t b0, uint32_t b1,
+                                          uint32_t id0, uint32_t id1, uint32_t accumulate) {
+#pragma unroll
+  for (uint32_t kk = 0; kk < BK / 16; ++kk) {
+    mma_pair_lo(d0, a0 + kk * K16<A_MN>, b0 + kk * K16<B_MN>, id0, kk == 0 ? accumulate : 1u);
+    if (TWO) mma_pair_lo(d1, a0 + kk * K16<A_MN>, b1 + kk * K16<B_MN>, id1, kk == 0 ? accumulate : 1u);
+  }
+}
+
+// Lane 0's values, for the compiler to hold in uniform registers.
+__device__ __forceinline__ Tile uniform(Tile t) {
+  t.e = __shfl_sync(0xffffffffu, t.e, 0);
+  t.f0 = __shfl_sync(0xffffffffu, t.f0, 0);
+  t.c0 = __shfl_sync(0xffffffffu, t.c0, 0);
+  t.cols = __shfl_sync(0xffffffffu, t.cols, 0);
+  t.halves = __shfl_sync(0xffffffffu, t.halves, 0);
+  t.nh = __shfl_sync(0xffffffffu, t.nh, 0);
+  t.depth = __shfl_sync(0xffffffffu, t.depth, 0);
+  t.r0 = __shfl_sync(0xffffffffu, t.r0, 0);
+  return t;
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+// A wait by the whole warp; all lanes agree on its outcome.
+__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t* err) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, err));
+}
+
+// FWD, DX: which box brings the valid rows among a CTA's n / 2 columns of a
+// half (-1: there are none), and its rows. What a box leaves of the columns
+// holds an earlier stage's rows; results of such columns are not stored. Rows
+// that are not needed are not read: a decode batch's 28 tiles of an expert
+// all read its few rows, and 32 rows a stage instead of 8 cost the V3
+// down-projection 18 % of its time.
+__device__ __forceinline__ int row_box(int cols, int n, int rank) {
+  const int need = min(cols - rank * (n / 2), n / 2);
+  return need <= 0 ? -1 : need <= 8 ? 0 : (need + 15) >> 4;
+}
+__device__ __forceinline__ int box_rows(int box) { return box < 0 ? 0 : box == 0 ? 8 : 16 * box; }
 
 // Stage of a tile: A, then the halves of B; the ring's position after it.
 template <int MODE> __device__ __forceinline__ uint32_t stage_bytes(const Tile& t) {
@@ -170,6 +230,59 @@ template <int MODE> struct Ring {
   __device__ __forceinline__ void advance(uint32_t b) {
     pos += b;
     if (++slot == SLOTS) { slot = 0; ph ^= 1; }
+  }
+};
+
+// The producer's account of the stages not yet known to be consumed, all in
+// registers: the oldest run of equal-sized stages and the newest (a tile's
+// stages are of one size), and where the oldest begins, as an offset into the
+// ring and as a running count of the bytes given out (differences only).
+template <int MODE> struct Outstanding {
+  uint32_t old_n = 0, old_sz = 0, new_n = 0, new_sz = 0;
+  uint32_t pos = 0, v = 0, vpos = 0;  // the oldest's offset and count; the next's count
+  uint32_t slot = 0, ph = 0;          // the oldest's barrier
+  __device__ __forceinline__ bool retire(uint64_t* empty, volatile int* abort_flag, uint32_t* err) {
+    if (!wait_all(&empty[slot], ph, abort_flag, err)) return false;
+    if (++slot == SLOTS) { slot = 0; ph ^= 1; }
+    pos += old_sz;
+    v += old_sz;
+    if (--old_n == 0) {
+      old_n = new_n;
+      old_sz = new_sz;
+      new_n = 0;
+    }
+    if (pos + old_sz > (uint32_t)Cfg<MODE>::RING) {  // the next began at the ring's start
+      v += Cfg<MODE>::RING - pos;
+      pos = 0;
+    }
+    return true;
+  }
+  // before a tile of stages of sz bytes: two runs at most
+  __device__ __forceinline__ bool begin(uint32_t sz, uint64_t* empty, volatile int* abort_flag, uint32_t* err) {
+    while (new_n > 0 && new_sz != sz)
+      if (!retire(empty, abort_flag, err)) return false;
+    return true;
+  }
+  // until `bytes` more (padding included) and a slot are free
+  __device__ __forceinline__ bool make_room(uint32_t bytes, uint64_t* empty, volatile int* abort_flag,
+                                            uint32_t* err) {
+    while (old_n > 0 && (old_n + new_n == SLOTS || vpos + bytes - v > (uint32_t)Cfg<MODE>::RING))
+      if (!retire(empty, abort_flag, err)) return false;
+    return true;
+  }
+  __device__ __forceinline__ void push(uint32_t sz, uint32_t at, uint32_t pad) {
+    if (old_n == 0) {
+      old_sz = sz;
+      pos = at;
+      v = vpos + pad;
+    }
+    if (new_n == 0 && old_sz == sz) {
+      ++old_n;
+    } else {
+      new_sz = sz;
+      ++new_n;
+    }
+    vpos += pad + sz;
   }
 };
 
@@ -201,7 +314,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* s_cap = reinterpret_cast<volatile int*>(tmem_slot + 2);
-  uint32_t* vstart = tmem_slot + 3;  // the producer's stage starts, [SLOTS]
   int32_t* cnt = reinterpret_cast<int32_t*>(stage_out + 8 * C::STG + 512);  // [E], then P [E + 1]
   int32_t* P = cnt + MAX_E;
 
@@ -305,125 +417,140 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
 
   if (warp == 0) {
     // ---------------------------------------------------------------- TMA producer (both CTAs)
-    if (lane == 0) {
-      Ring<MODE> R;
-      // stages issued and known to be consumed; bytes of the ring given out,
-      // padding included (differences only: both may wrap)
-      uint32_t issued = 0, done = 0, vpos = 0, dslot = 0, dph = 0;
-      int last_e = -1;
-      bool ok = true;
-      for (int i = pair; ok && i < S.total; i += npairs) {
-        const Tile t = decode<MODE>(S, i);
-        const int kb_n = (t.depth + BK - 1) / BK;
-        if (kb_n == 0) continue;
-        const uint32_t sz = stage_bytes<MODE>(t);
-        const int f = t.f0 + (int)rank * FM;
-        // this CTA's N columns of each half: [c0 + h nh + rank n/2, + n/2)
-        const int n0 = half_n(t, 0), n1 = t.halves == 2 ? half_n(t, 1) : 0;
-        const int cb0 = t.c0 + (int)rank * (n0 / 2), cb1 = t.c0 + t.nh + (int)rank * (n1 / 2);
-        const CUtensorMap *ma = &g.tmA, *mb0 = nullptr, *mb1 = nullptr;
-        uint32_t tx = 2u * TILE;
-        if (MODE == GMM_DW) {
-          ma = g.maps + t.e;
-          mb0 = g.maps + E + t.e;
-          if (t.e != last_e) {
-            tmap_acquire(ma);
-            tmap_acquire(mb0);
-            last_e = t.e;
-          }
-          tx += 2u * TILE;
-        } else {
-          mb0 = &g.tmB[n0 / 32 - 1];
-          if (t.halves == 2) mb1 = &g.tmB[n1 / 32 - 1];
-          tx += (uint32_t)(n0 + n1) * (BK * 2);
+    // The whole warp runs the loop on warp-uniform values and one lane issues:
+    // the copies' operands then come from uniform registers. No shared memory
+    // is read per stage (a load would queue behind the copies, ~230 cycles).
+    const bool el = elect_one();
+    Ring<MODE> R;
+    Outstanding<MODE> Q;
+    uint32_t issued = 0;
+    int last_e = -1;
+    bool ok = true;
+    for (int i = pair; ok && i < S.total; i += npairs) {
+      const Tile t = uniform(decode<MODE>(S, i));
+      const int kb_n = (t.depth + BK - 1) / BK;
+      if (kb_n == 0) continue;
+      const uint32_t sz = stage_bytes<MODE>(t);
+      const int f = t.f0 + (int)rank * FM;
+      // this CTA's N columns of each half: [c0 + h nh + rank n/2, + n/2)
+      const int n0 = half_n(t, 0), n1 = t.halves == 2 ? half_n(t, 1) : 0;
+      const int cb0 = t.c0 + (int)rank * (n0 / 2), cb1 = t.c0 + t.nh + (int)rank * (n1 / 2);
+      const CUtensorMap *ma = &g.tmA, *mb0 = g.maps + E + t.e, *mb1 = nullptr;
+      uint32_t tx = 2u * TILE;
+      bool ld0 = true, ld1 = false;
+      if (MODE == GMM_DW) {
+        ma = g.maps + t.e;
+        if (t.e != last_e) {
+          tmap_acquire(ma);
+          tmap_acquire(mb0);
+          last_e = t.e;
         }
-        for (int kb = 0; kb < kb_n; ++kb) {
-          uint8_t* sa = tiles + R.place(sz);
+        tx += 2u * TILE;
+      } else {
+        const int c0 = min(t.cols, t.nh), c1 = t.cols - c0;  // valid columns of the halves
+        const int x0 = row_box(c0, n0, rank), x1 = t.halves == 2 ? row_box(c1, n1, rank) : -1;
+        ld0 = x0 >= 0;
+        ld1 = x1 >= 0;
+        mb0 = &g.tmB[max(x0, 0)];
+        mb1 = &g.tmB[max(x1, 0)];
+        int rows = box_rows(row_box(c0, n0, 0)) + box_rows(row_box(c0, n0, 1));
+        if (t.halves == 2) rows += box_rows(row_box(c1, n1, 0)) + box_rows(row_box(c1, n1, 1));
+        tx += (uint32_t)rows * (BK * 2);
+      }
+      ok = Q.begin(sz, empty, abort_flag, g.err);
+      for (int kb = 0; ok && kb < kb_n; ++kb) {
+        const uint32_t at = R.place(sz);
+        if (!Q.make_room(R.pad + sz, empty, abort_flag, g.err)) { ok = false; break; }
+        Q.push(sz, at, R.pad);
+        if (el) {
+          uint8_t* sa = tiles + at;
           uint8_t* sb = sa + TILE;
-          const uint32_t vend = vpos + R.pad + sz;
-          // the oldest stages out of the way: a slot and the bytes
-          while (issued != done && (issued - done == SLOTS || vend - vstart[dslot] > (uint32_t)C::RING)) {
-            if (!mbar_wait(&empty[dslot], dph, abort_flag, g.err)) { ok = false; break; }
-            ++done;
-            if (++dslot == SLOTS) { dslot = 0; dph ^= 1; }
-          }
-          if (!ok) break;
-          vstart[R.slot] = vpos + R.pad;
-          vpos = vend;
           const uint32_t fb = mapa(smem_u32(&full[R.slot]), 0);
           if (leader) mbar_expect_tx(&full[R.slot], tx);
           const int kk = kb * BK;
           if (MODE == GMM_FWD) {
             tma2_load_3d(sa, ma, fb, kk, f, t.e);
           } else if (MODE == GMM_DX) {
-            tma2_load_3d(sa, ma, fb, f, kk, t.e);
-            tma2_load_3d(sa + TILE / 2, ma, fb, f + 64, kk, t.e);
+            if (g.wide) {
+              tma2_load_4d(sa, ma, fb, 0, kk, f / 64, t.e);
+            } else {
+              tma2_load_3d(sa, ma, fb, f, kk, t.e);
+              tma2_load_3d(sa + TILE / 2, ma, fb, f + 64, kk, t.e);
+            }
           } else {
-            tma2_load_2d(sa, ma, fb, f, t.r0 + kk);
-            tma2_load_2d(sa + TILE / 2, ma, fb, f + 64, t.r0 + kk);
-          }
-          if (MODE == GMM_DW) {
             const int c = t.c0 + (int)rank * (t.nh / 2);
+            if (g.wide) {
+              tma2_load_4d(sa, ma, fb, 0, t.r0 + kk, f / 64, 0);
+            } else {
+              tma2_load_2d(sa, ma, fb, f, t.r0 + kk);
+              tma2_load_2d(sa + TILE / 2, ma, fb, f + 64, t.r0 + kk);
+            }
             tma2_load_2d(sb, mb0, fb, c, t.r0 + kk);
             tma2_load_2d(sb + TILE / 2, mb0, fb, c + 64, t.r0 + kk);
-          } else {
-            tma2_load_2d(sb, mb0, fb, kk, cb0);
-            if (mb1) tma2_load_2d(sb + n0 * BK, mb1, fb, kk, cb1);
           }
-          ++issued;
-          R.advance(sz);
+          if (MODE != GMM_DW) {
+            if (ld0) tma2_load_2d(sb, mb0, fb, kk, cb0);
+            if (ld1) tma2_load_2d(sb + n0 * BK, mb1, fb, kk, cb1);
+          }
         }
+        ++issued;
+        R.advance(sz);
       }
-      if (!ok && leader)
-        for (uint32_t j = 0; j < SLOTS; ++j) {
-          const uint32_t n = issued / SLOTS + (j < issued % SLOTS ? 1 : 0);
-          if (n > 0) mbar_drain(&full[j], (n - 1) & 1);
-        }
     }
+    if (!ok && leader && el)
+      for (uint32_t j = 0; j < SLOTS; ++j) {
+        const uint32_t n = issued / SLOTS + (j < issued % SLOTS ? 1 : 0);
+        if (n > 0) mbar_drain(&full[j], (n - 1) & 1);
+      }
+    __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer (leader)
-    if (leader && lane == 0) {
+    if (leader) {
+      const bool el = elect_one();
       Ring<MODE> R;
-      uint32_t hb = 0;  // hb: halves so far; half i uses accumulator i & 1
+      const uint32_t tiles0 = smem_u32(tiles);
+      uint32_t hb = 0;  // halves so far; half i uses accumulator i & 1
       bool ok = true;
-      if (g.stall && blockIdx.x == 0 && !mbar_wait(drain, 0, abort_flag, g.err)) ok = false;
+      if (g.stall && blockIdx.x == 0) ok = wait_all(drain, 0, abort_flag, g.err);
       for (int i = pair; ok && i < S.total; i += npairs) {
-        const Tile t = decode<MODE>(S, i);
+        const Tile t = uniform(decode<MODE>(S, i));
         const int kb_n = (t.depth + BK - 1) / BK;
         if (kb_n == 0) continue;
         const uint32_t sz = stage_bytes<MODE>(t), b1 = (uint32_t)half_n(t, 0) * BK;
         constexpr uint32_t MAJ = (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
         const uint32_t id0 = idesc_bf16(2 * FM, half_n(t, 0)) | MAJ;
         const uint32_t id1 = t.halves == 2 ? idesc_bf16(2 * FM, half_n(t, 1)) | MAJ : 0u;
-        uint32_t d[2];
-        for (int h = 0; ok && h < t.halves; ++h) {
-          const uint32_t u = hb + h;
-          ok = mbar_wait(&tempty[u & 1], ((u >> 1) & 1) ^ 1, abort_flag, g.err);
-          d[h] = tmem_base + (u & 1) * MAXN;
-        }
-        if (!ok) break;
+        const uint32_t d0 = tmem_base + (hb & 1) * MAXN, d1 = tmem_base + (~hb & 1) * MAXN;
+        if (!wait_all(&tempty[hb & 1], ((hb >> 1) & 1) ^ 1, abort_flag, g.err)) break;
+        if (t.halves == 2 && !wait_all(&tempty[~hb & 1], (((hb + 1) >> 1) & 1) ^ 1, abort_flag, g.err))
+          break;
         tc_fence_after();
         for (int kb = 0; kb < kb_n; ++kb) {
-          const uint32_t a0 = smem_u32(tiles) + R.place(sz);
-          if (!mbar_wait(&full[R.slot], R.ph, abort_flag, g.err)) { ok = false; break; }
+          const uint32_t st = tiles0 + R.place(sz);
+          if (!wait_all(&full[R.slot], R.ph, abort_flag, g.err)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t b0 = a0 + TILE;
-#pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk) {
-            const uint64_t ad = desc_k16<A_MN>(a0, kk);
-            mma_pair(d[0], ad, desc_k16<B_MN>(b0, kk), id0, (kb | kk) != 0 ? 1u : 0u);
+          if (el) {
+            const uint32_t al = desc_lo<A_MN>(st), bl = desc_lo<B_MN>(st + TILE);
             if (C::HALVES == 2 && t.halves == 2)
-              mma_pair(d[1], ad, desc_k16<B_MN>(b0 + b1, kk), id1, (kb | kk) != 0 ? 1u : 0u);
+              mma_stage<A_MN, B_MN, true>(d0, d1, al, bl, bl + (b1 >> 4), id0, id1, kb > 0);
+            else
+              mma_stage<A_MN, B_MN, false>(d0, 0, al, bl, 0, id0, 0, kb > 0);
+            commit_pair(&empty[R.slot]);
           }
-          commit_pair(&empty[R.slot]);
           R.advance(sz);
         }
         if (!ok) break;
-        for (int h = 0; h < t.halves; ++h) commit_pair(&tfull[(hb + h) & 1]);
+        if (el) {
+          commit_pair(&tfull[hb & 1]);
+          if (t.halves == 2) commit_pair(&tfull[~hb & 1]);
+        }
         hb += t.halves;
       }
-      commit_pair(drain);
-      mbar_drain(drain, 0);
+      if (el) {
+        commit_pair(drain);
+        mbar_drain(drain, 0);
+      }
+      __syncwarp();
     }
   } else {
     // ---------------------------------------------------------------- epilogue (both CTAs)
@@ -601,6 +728,21 @@ bool map_rows(CUtensorMap* m, const void* p, int64_t rows, int cols, uint32_t bo
   return tc::map_2d(m, p, (uint64_t)rows, (uint64_t)cols, box);
 }
 
+// Stacked matrices [E, rows, cols], cols a multiple of 64, as {64, rows, cols
+// / 64, E}: a box of 64 rows x 128 columns is two 8 KB MN-major boxes in one
+// copy.
+bool map_chunks(CUtensorMap* m, const void* p, int64_t E, int64_t rows, int64_t cols) {
+  auto fn = tc::encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[4] = {64, (cuuint64_t)rows, (cuuint64_t)(cols / 64), (cuuint64_t)E};
+  cuuint64_t strides[3] = {(cuuint64_t)cols * 2, 128, (cuuint64_t)(rows * cols * 2)};
+  cuuint32_t box[4] = {64, BK, FM / 64, 1};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(p), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // dw [E, n, k] in boxes of 128 bytes x 32 outputs, for stores.
 bool map_out(CUtensorMap* m, const void* p, int E, int n, int k, bool f32) {
   auto fn = tc::encode_fn();
@@ -625,7 +767,9 @@ cudaError_t launch(const GmmArgs& a, void* maps, int num_sms, cudaStream_t st) {
     if (a.rows > 0) {
       EndMapArgs m;
       m.maps = static_cast<CUtensorMap*>(maps);
-      if (!map_rows(&m.base[0], a.a, a.rows, a.n, BK) || !map_rows(&m.base[1], a.b, a.rows, a.k, BK))
+      g.wide = a.n % 64 == 0;
+      if (!(g.wide ? map_chunks(&m.base[0], a.a, 1, a.rows, a.n) : map_rows(&m.base[0], a.a, a.rows, a.n, BK)) ||
+          !map_rows(&m.base[1], a.b, a.rows, a.k, BK))
         return cudaErrorInvalidValue;
       gmm_end_maps_kernel<<<dim3((unsigned)ceil_div(a.E, 8), 2), 256, 0, st>>>(m, a.offsets, a.rows, a.E);
       const cudaError_t e = cudaGetLastError();
@@ -635,10 +779,13 @@ cudaError_t launch(const GmmArgs& a, void* maps, int num_sms, cudaStream_t st) {
     if (!map_out(&g.tmO, a.out, a.E, a.n, a.k, a.out_f32)) return cudaErrorInvalidValue;
   } else {
     if (a.rows == 0) return cudaSuccess;
-    if (!tc::map_3d(&g.tmA, a.b, (uint64_t)a.E, (uint64_t)a.n, (uint64_t)a.k, MODE == GMM_FWD ? FM : BK))
+    g.wide = MODE == GMM_DX && a.k % 64 == 0;
+    if (!(g.wide ? map_chunks(&g.tmA, a.b, a.E, a.n, a.k)
+                 : tc::map_3d(&g.tmA, a.b, (uint64_t)a.E, (uint64_t)a.n, (uint64_t)a.k,
+                              MODE == GMM_FWD ? FM : BK)))
       return cudaErrorInvalidValue;
     for (int i = 0; i < NBOX; ++i)
-      if (!map_rows(&g.tmB[i], a.a, a.rows, MODE == GMM_FWD ? a.k : a.n, 16 * (i + 1)))
+      if (!map_rows(&g.tmB[i], a.a, a.rows, MODE == GMM_FWD ? a.k : a.n, i == 0 ? 8 : 16 * i))
         return cudaErrorInvalidValue;
   }
   g.out = a.out;
