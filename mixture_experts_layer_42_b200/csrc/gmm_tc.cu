@@ -19,13 +19,14 @@
 // over the boxes (64 features), its stride over 8 reduction rows.
 //
 // Stages of the shared-memory ring are as large as their tile's operands, so
-// that the same 200 KB hold 11 stages of a decode tile and 4 of a tile of 512
+// that the same 192 KB hold 10 stages of a decode tile and 4 of a tile of 512
 // rows: what covers the memory's latency is bytes in flight.
 //
-// Per CTA, 320 threads: warp 0 the TMA producer, warp 1 of the pair's leader
+// Per CTA, 352 threads: warp 0 the TMA producer, warp 1 of the pair's leader
 // the MMA issuer, warps 2-9 the epilogue (two warps on each 32 TMEM lanes, in
-// turn over the columns). dw leaves through shared memory by TMA stores, or
-// TMA additions to a fp32 dw that is accumulated into. Rows of a tile past its expert's
+// turn over the columns), warp 10 the scheduler, which works the tiles out
+// ahead of the others. Results leave through a warp's own shared memory, so
+// that a store instruction covers whole sectors of a few rows. Rows of a tile past its expert's
 // end are other rows of the matrix (their columns are not stored); only DW,
 // which sums over rows, reads through per-expert maps that end at the
 // expert's last row. Every wait is bounded (1 s); on expiry the kernel raises
@@ -45,25 +46,29 @@ constexpr int BK = 64;                    // reduction depth of a stage (128 byt
 constexpr int FM = 128;                   // features per CTA; a pair holds 256
 constexpr int MAXN = 256;                 // N columns of one half
 constexpr int TILE = FM * BK * 2;         // 16 KB: an operand tile of a stage
-constexpr int NUM_THREADS = 320;
+constexpr int NUM_THREADS = 352;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int MAX_E = 1024;
 constexpr int NBOX = 9;                   // row boxes of 8, 16, 32, 48, ... 128 rows
 constexpr int SLOTS = 12;                 // stages in flight, at most
+constexpr int TQ = 4;                     // tiles the scheduler works out ahead
+constexpr int HEAVY = 256;                // rows above which an expert's tiles count as heavy
 
 template <int MODE> struct Cfg {
   static constexpr int HALVES = MODE == GMM_DW ? 1 : 2;
-  static constexpr int RING = MODE == GMM_DW ? 5 * 2 * TILE : 200 * 1024;
-  // staging of an epilogue warp: DW 32 rows of 128 bytes for a TMA store, else
-  // 32 rows x 32 bf16
+  static constexpr int RING = MODE == GMM_DW ? 5 * 2 * TILE : 192 * 1024;
+  // staging of an epilogue warp: DW 32 outputs x 32 inputs in fp32, else 32
+  // rows x 32 features in bf16
   static constexpr int STG = MODE == GMM_DW ? 4096 : 2048;
-  static constexpr size_t SMEM = 1024 + RING + 8 * STG + 512 + (2 * MAX_E + 1) * 4;
+  // experts' first rows and counts, and (FWD, DX) the tile prefixes of the
+  // heavy and of the light ones
+  static constexpr int TABLE = (MODE == GMM_DW ? 2 : 4) * (MAX_E + 1) * 4;
+  static constexpr size_t SMEM = 1024 + RING + 8 * STG + 512 + TABLE;
 };
 
 struct TcGmm {
   CUtensorMap tmA;          // FWD, DX: the weights
   CUtensorMap tmB[NBOX];    // FWD, DX: the rows, boxes of 8, 16, 32, 48, ... 128 rows
-  CUtensorMap tmO;          // DW: dw, in boxes of 128 bytes x 32 outputs
   const CUtensorMap* maps;  // DW: [2, E] maps of dy and of x ending at each expert's last row
   void* out;
   const int32_t* offsets;
@@ -77,7 +82,7 @@ struct TcGmm {
 
 // M features (over both CTAs of the pair), N columns and reduction depth.
 struct Tile {
-  int e;
+  int e;       // expert; -1: no more tiles
   int f0;      // first of the pair's 256 features
   int c0;      // first N column: row of the matrix (FWD, DX) or input (DW)
   int cols;    // valid N columns
@@ -87,17 +92,23 @@ struct Tile {
   int r0;      // DW: the expert's first row
 };
 
-// FWD, DX: expert e's rows in mt tiles of `per` rows.
 struct Sched {
-  const int32_t* P;    // smem: token-tile prefix over experts [E + 1]
-  const int32_t* off;  // smem: first row of each expert [E + 1]; count in P's companion
+  const int32_t* off;  // smem: first row and number of rows of each expert
   const int32_t* cnt;
-  int E, nf, nc, total, cap, n, k;
+  const int32_t* PH;   // smem: token-tile prefixes over experts [E + 1], of the heavy ones
+  const int32_t* PL;   // and of the light ones (FWD, DX)
+  int E, nf, nc, heavy, total, n, k;
 };
 
 __device__ __forceinline__ int round32(int v) { return (v + 31) & ~31; }
 __device__ __forceinline__ int tile_rows(int count, int mt) { return round32((count + mt - 1) / mt); }
 
+// Tile i of the launch. DW: expert by expert. FWD, DX: the tiles of the heavy
+// experts (many rows: bound by the MMAs) and of the light ones (few: bound by
+// their weights' bytes) in even turns, so that both run at any time and the
+// pairs' mixtures are alike; within each, expert by expert, its feature
+// blocks, and the row tiles that share them side by side (expert e's rows in
+// mt tiles of tile_rows each).
 template <int MODE>
 __device__ __forceinline__ Tile decode(const Sched& S, int i) {
   Tile t;
@@ -113,15 +124,19 @@ __device__ __forceinline__ Tile decode(const Sched& S, int i) {
     t.depth = S.cnt[t.e];
     t.r0 = S.off[t.e];
   } else {
+    const int h1 = (int)((int64_t)(i + 1) * S.heavy / S.total);  // heavy tiles up to and with i
+    const bool hv = h1 > (int)((int64_t)i * S.heavy / S.total);
+    const int32_t* P = hv ? S.PH : S.PL;
+    i = hv ? h1 - 1 : i - h1;
     const int q = i / S.nf;
     int lo = 0, hi = S.E;  // the e with P[e] <= q < P[e + 1]
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (S.P[mid] <= q) lo = mid; else hi = mid;
+      if (P[mid] <= q) lo = mid; else hi = mid;
     }
     t.e = lo;
-    const int mt = S.P[lo + 1] - S.P[lo];
-    const int l = i - S.nf * S.P[lo];
+    const int mt = P[lo + 1] - P[lo];
+    const int l = i - S.nf * P[lo];
     t.f0 = l / mt * (2 * FM);
     const int c = S.cnt[lo], per = tile_rows(c, mt), m = l % mt;
     t.c0 = S.off[lo] + m * per;
@@ -193,6 +208,20 @@ __device__ __forceinline__ bool elect_one() {
 __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t* err) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, err));
 }
+
+// A role's place in the scheduler's queue of tiles. next() reads a tile for
+// the whole warp; false on an abort or when there are no more.
+struct TileQueue {
+  uint32_t q = 0, ph = 0;
+  __device__ __forceinline__ bool next(Tile& t, const Tile* tq, uint64_t* qfull, uint64_t* qempty, int lane,
+                                       volatile int* abort_flag, uint32_t* err) {
+    if (!wait_all(&qfull[q], ph, abort_flag, err)) return false;
+    t = uniform(tq[q]);
+    if (lane == 0) mbar_arrive(&qempty[q]);
+    if (++q == TQ) { q = 0; ph ^= 1; }
+    return t.e >= 0;
+  }
+};
 
 // FWD, DX: which box brings the valid rows among a CTA's n / 2 columns of a
 // half (-1: there are none), and its rows. What a box leaves of the columns
@@ -286,16 +315,44 @@ template <int MODE> struct Outstanding {
   }
 };
 
-__device__ __forceinline__ void tma_store_3d(const CUtensorMap* tm, const void* src, int c0, int c1, int c2) {
-  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(tm),
-               "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
-               : "memory");
+// Arrive on the leader's barrier that an accumulator's columns have been read.
+// Relaxed: what it orders is the TMEM reads (tcgen05.wait::ld has completed
+// them, tcgen05.fence::before_thread_sync precedes it); a release would also
+// wait until L2 has taken the result's stores, ~3300 cycles a tile.
+__device__ __forceinline__ void arrive_read(uint32_t remote_bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote_bar) : "memory");
 }
-__device__ __forceinline__ void tma_add_3d(const CUtensorMap* tm, const void* src, int c0, int c1, int c2) {
-  asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
-                   tm),
-               "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
-               : "memory");
+
+// A warp's 32 x 32 block of dw from its staging (fp32, 16-byte places swizzled
+// by row), row and column bounds nr and nc: whole 128-byte rows of fp32 or 64
+// bytes of bf16 per store, added to what is there in fp32 when ACC.
+template <typename T, bool ACC>
+__device__ __forceinline__ void store_dw(const float4* stg, T* out, int64_t ld, int nr, int nc, int lane) {
+  constexpr int V = sizeof(T) == 4 ? 1 : 2;    // float4s a lane takes
+  constexpr int LPR = 8 / V, RPI = 32 / LPR;   // lanes per row, rows per instruction
+  const int c = lane % LPR * V;
+#pragma unroll
+  for (int it = 0; it < 32 / RPI; ++it) {
+    const int r = it * RPI + lane / LPR;
+    if (r >= nr || c * 4 >= nc) continue;
+    float f[4 * V];
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+      const float4 v = stg[r * 8 + ((c + u) ^ (r & 7))];
+      f[4 * u] = v.x; f[4 * u + 1] = v.y; f[4 * u + 2] = v.z; f[4 * u + 3] = v.w;
+    }
+    T* p = out + (int64_t)r * ld + c * 4;
+    Vec16<T> v;
+    if (ACC) {
+      float old[4 * V];
+      v.raw = *reinterpret_cast<const uint4*>(p);
+      v.to_float(old);
+#pragma unroll
+      for (int j = 0; j < 4 * V; ++j) f[j] += old[j];
+    }
+    v.from_float(f);
+    *reinterpret_cast<uint4*>(p) = v.raw;
+  }
 }
 
 template <int MODE>
@@ -311,11 +368,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
   uint64_t* tfull = empty + SLOTS;
   uint64_t* tempty = tfull + 2;
   uint64_t* drain = tempty + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* qfull = drain + 1;
+  uint64_t* qempty = qfull + TQ;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(qempty + TQ);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  volatile int* s_cap = reinterpret_cast<volatile int*>(tmem_slot + 2);
-  int32_t* cnt = reinterpret_cast<int32_t*>(stage_out + 8 * C::STG + 512);  // [E], then P [E + 1]
-  int32_t* P = cnt + MAX_E;
+  Tile* tq = reinterpret_cast<Tile*>(tmem_slot + 4);  // [TQ]
+  int32_t* cnt = reinterpret_cast<int32_t*>(stage_out + 8 * C::STG + 512);
+  int32_t* off = cnt + MAX_E + 1;
+  int32_t* PH = off + MAX_E + 1;
+  int32_t* PL = PH + MAX_E + 1;
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t rank = cluster_rank();
@@ -331,6 +392,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       // tempty: one arrive per epilogue warp of both CTAs (used on the leader)
       for (int a = 0; a < 2; ++a) { mbar_init(&tfull[a], 1); mbar_init(&tempty[a], 16); }
       mbar_init(drain, 1);
+      // read by the epilogue warps, the producer and the leader's MMA issuer
+      for (int q = 0; q < TQ; ++q) { mbar_init(&qfull[q], 1); mbar_init(&qempty[q], leader ? 10 : 9); }
       *abort_flag = 0;
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -338,6 +401,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     const int per = (E + 31) / 32;
     bool bad = false;
     int maxc = 0;
+    int64_t rows = 0;
     int tl[5] = {0, 0, 0, 0, 0};  // tiles at a cap of 512, 256, 128, 64, 32 rows
     for (int u = 0; u < per; ++u) {
       const int e = lane * per + u;
@@ -345,51 +409,61 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         const Span s = expert_span(g.offsets, e, g.rows);
         bad |= s.bad;
         cnt[e] = s.count;
+        off[e] = s.b;
         maxc = max(maxc, s.count);
+        rows += s.count;
 #pragma unroll
         for (int c = 0; c < 5; ++c) tl[c] += (int)(((int64_t)s.count + (512 >> c) - 1) >> (9 - c));
       }
     }
     if (bad && blockIdx.x == 0) set_error(g.err, ERRBIT_BAD_INDEX);
-    int cap = 512;
     if (MODE != GMM_DW) {
-      // The rows a tile may hold. Two costs decide: a tile's traffic and MMA
-      // time, about 256 + rows, and how evenly the tiles fill the pairs.
+      // The rows a tile may hold. What bounds large calls is the traffic from
+      // L2, 256 + rows per tile and 64 of the reduction, shared by the pairs;
+      // a small call also waits for its last tile, up to 256 + cap.
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) {
         maxc = max(maxc, __shfl_xor_sync(0xffffffffu, maxc, o));
+        rows += __shfl_xor_sync(0xffffffffu, rows, o);
 #pragma unroll
         for (int c = 0; c < 5; ++c) tl[c] += __shfl_xor_sync(0xffffffffu, tl[c], o);
       }
+      int cap = 512;
       int64_t best = INT64_MAX;
 #pragma unroll
       for (int c = 0; c < 5; ++c) {
-        const int64_t waves = ((int64_t)tl[c] * nf + npairs - 1) / npairs;
-        const int64_t cost = waves * (256 + min(512 >> c, round32(maxc)));
+        const int most = 256 + min(512 >> c, round32(maxc));
+        const int64_t all = ((int64_t)tl[c] * 256 + rows) * nf / npairs;
+        const int64_t cost = tl[c] * (int64_t)nf <= npairs ? most : all + most;
         if (cost < best) { best = cost; cap = 512 >> c; }
       }
-      int lsum = 0;
+      int sum[2] = {0, 0};  // token tiles of this lane's light and heavy experts
       for (int u = 0; u < per; ++u) {
         const int e = lane * per + u;
-        if (e < E) lsum += (int)(((int64_t)cnt[e] + cap - 1) / cap);
+        if (e < E) sum[cnt[e] > HEAVY] += (int)(((int64_t)cnt[e] + cap - 1) / cap);
       }
-      int incl = lsum;
+      int run[2];
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int p = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += p;
+      for (int h = 0; h < 2; ++h) {
+        int incl = sum[h];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int p = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += p;
+        }
+        run[h] = incl - sum[h];
+        if (lane == 31) (h ? PH : PL)[E] = incl;
       }
-      int run = incl - lsum;
       for (int u = 0; u < per; ++u) {
         const int e = lane * per + u;
         if (e < E) {
-          P[e] = run;
-          run += (int)(((int64_t)cnt[e] + cap - 1) / cap);
+          PL[e] = run[0];
+          PH[e] = run[1];
+          const int mt = (int)(((int64_t)cnt[e] + cap - 1) / cap);
+          if (cnt[e] > HEAVY) run[1] += mt; else run[0] += mt;
         }
       }
-      if (lane == 31) P[E] = incl;
     }
-    if (lane == 0) *s_cap = cap;
     __syncwarp();
   } else if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -404,16 +478,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
   const uint32_t tmem_base = *tmem_slot;
 
   Sched S;
-  S.P = P;
-  S.off = g.offsets;
+  S.off = off;
   S.cnt = cnt;
+  S.PH = PH;
+  S.PL = PL;
   S.E = E;
   S.nf = nf;
   S.nc = (g.k + MAXN - 1) / MAXN;
-  S.cap = *s_cap;
   S.n = g.n;
   S.k = g.k;
-  S.total = MODE == GMM_DW ? E * nf * S.nc : nf * P[E];
+  S.heavy = MODE == GMM_DW ? 0 : nf * PH[E];
+  S.total = MODE == GMM_DW ? E * nf * S.nc : S.heavy + nf * PL[E];
 
   if (warp == 0) {
     // ---------------------------------------------------------------- TMA producer (both CTAs)
@@ -426,8 +501,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     uint32_t issued = 0;
     int last_e = -1;
     bool ok = true;
-    for (int i = pair; ok && i < S.total; i += npairs) {
-      const Tile t = uniform(decode<MODE>(S, i));
+    TileQueue T;
+    Tile t;
+    while (ok && T.next(t, tq, qfull, qempty, lane, abort_flag, g.err)) {
       const int kb_n = (t.depth + BK - 1) / BK;
       if (kb_n == 0) continue;
       const uint32_t sz = stage_bytes<MODE>(t);
@@ -497,7 +573,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         R.advance(sz);
       }
     }
-    if (!ok && leader && el)
+    if (*abort_flag && leader && el)
       for (uint32_t j = 0; j < SLOTS; ++j) {
         const uint32_t n = issued / SLOTS + (j < issued % SLOTS ? 1 : 0);
         if (n > 0) mbar_drain(&full[j], (n - 1) & 1);
@@ -512,8 +588,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       uint32_t hb = 0;  // halves so far; half i uses accumulator i & 1
       bool ok = true;
       if (g.stall && blockIdx.x == 0) ok = wait_all(drain, 0, abort_flag, g.err);
-      for (int i = pair; ok && i < S.total; i += npairs) {
-        const Tile t = uniform(decode<MODE>(S, i));
+      TileQueue T;
+      Tile t;
+      while (ok && T.next(t, tq, qfull, qempty, lane, abort_flag, g.err)) {
         const int kb_n = (t.depth + BK - 1) / BK;
         if (kb_n == 0) continue;
         const uint32_t sz = stage_bytes<MODE>(t), b1 = (uint32_t)half_n(t, 0) * BK;
@@ -552,18 +629,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       }
       __syncwarp();
     }
+  } else if (warp == 10) {
+    // ---------------------------------------------------------------- scheduler (both CTAs)
+    uint32_t q = 0, ph = 0;
+    for (int i = pair;; i += npairs) {
+      Tile t;
+      t.e = -1;
+      if (i < S.total) t = decode<MODE>(S, i);
+      if (!wait_all(&qempty[q], ph ^ 1, abort_flag, g.err)) break;
+      if (lane == 0) {
+        tq[q] = t;
+        mbar_arrive(&qfull[q]);
+      }
+      if (t.e < 0) break;
+      if (++q == TQ) { q = 0; ph ^= 1; }
+    }
   } else {
     // ---------------------------------------------------------------- epilogue (both CTAs)
     const int quad = warp & 3, cg = (warp - 2) >> 2;  // TMEM lanes, turn over the columns
     const uint32_t free_bar[2] = {mapa(smem_u32(&tempty[0]), 0), mapa(smem_u32(&tempty[1]), 0)};
     uint8_t* stg = stage_out + (warp - 2) * C::STG;
-    // columns a warp takes at once
-    const int step = MODE == GMM_DW && !g.out_f32 ? 64 : 32;
-    const bool direct = MODE == GMM_DW && g.accumulate && !g.out_f32;
     uint32_t hb = 0;
     int ok = 1;
-    for (int i = pair; ok && i < S.total; i += npairs) {
-      const Tile t = decode<MODE>(S, i);
+    TileQueue T;
+    Tile t;
+    while (ok && T.next(t, tq, qfull, qempty, lane, abort_flag, g.err)) {
       const int fw = t.f0 + (int)rank * FM + quad * 32;  // this warp's first feature
       const bool zero = t.depth == 0;  // DW of an expert without rows
       if (zero && g.accumulate) continue;
@@ -578,9 +668,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         const int nv = min(t.cols - h * t.nh, t.nh);  // valid columns of this half
         const int cb = t.c0 + h * t.nh;
 #pragma unroll 1
-        for (int c = cg * step; c < nv; c += 2 * step) {
+        for (int c = cg * 32; c < nv; c += 64) {
           uint32_t r[32];
-          __syncwarp();
+          __syncwarp();  // (the staging's last reads)
           if (!zero) {
             tmem_ld16(tb + c, *reinterpret_cast<uint32_t(*)[16]>(r));
             tmem_ld16(tb + c + 16, *reinterpret_cast<uint32_t(*)[16]>(r + 16));
@@ -589,71 +679,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
             for (int j = 0; j < 32; ++j) r[j] = 0;
           }
-          if (MODE == GMM_DW && !direct) {
-            // lane = output row of dw; 128 bytes of inputs through shared
-            // memory (16-byte places swizzled by row) and a TMA store
-            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-            __syncwarp();
+          if (MODE == GMM_DW) {
+            // lane = output row of dw, 32 inputs
             uint4* row = reinterpret_cast<uint4*>(stg + lane * 128);
-            if (g.out_f32) {
 #pragma unroll
-              for (int j = 0; j < 8; ++j)
-                row[j ^ (lane & 7)] = make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
-            } else {
-#pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                if (u == 1 && !zero) {
-                  tmem_ld16(tb + c + 32, *reinterpret_cast<uint32_t(*)[16]>(r));
-                  tmem_ld16(tb + c + 48, *reinterpret_cast<uint32_t(*)[16]>(r + 16));
-                  tmem_wait_ld();
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  Vec16<__nv_bfloat16> v;
-                  v.from_float(reinterpret_cast<const float*>(r) + 8 * j);
-                  row[(u * 4 + j) ^ (lane & 7)] = v.raw;
-                }
-              }
-            }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            for (int j = 0; j < 8; ++j)
+              row[j ^ (lane & 7)] = make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
             __syncwarp();
-            if (lane == 0 && fw < NF) {
-              if (g.accumulate) tma_add_3d(&g.tmO, stg, cb + c, fw, t.e);
-              else tma_store_3d(&g.tmO, stg, cb + c, fw, t.e);
-              asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-            }
-          } else if (MODE == GMM_DW) {
-            // accumulation into a bf16 dw: its values in fp32, one rounding
-            // (the TMEM loads are the whole warp's, whatever its rows)
-            const int64_t o = ((int64_t)t.e * g.n + fw + lane) * g.k + cb + c;
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              if (c + u * 32 >= nv) break;
-              if (u == 1) {
-                tmem_ld16(tb + c + 32, *reinterpret_cast<uint32_t(*)[16]>(r));
-                tmem_ld16(tb + c + 48, *reinterpret_cast<uint32_t(*)[16]>(r + 16));
-                tmem_wait_ld();
-              }
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                if (fw + lane >= NF || c + u * 32 + q * 8 >= nv) continue;  // k is a multiple of 8
-                __nv_bfloat16* p = static_cast<__nv_bfloat16*>(g.out) + o + u * 32 + q * 8;
-                Vec16<__nv_bfloat16> v;
-                float old[8];
-                v.raw = *reinterpret_cast<const uint4*>(p);
-                v.to_float(old);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) old[j] += __uint_as_float(r[q * 8 + j]);
-                v.from_float(old);
-                *reinterpret_cast<uint4*>(p) = v.raw;
-              }
-              __syncwarp();
+            const float4* blk = reinterpret_cast<const float4*>(stg);
+            const int64_t o = ((int64_t)t.e * g.n + fw) * g.k + cb + c;
+            if (g.out_f32) {
+              float* p = static_cast<float*>(g.out) + o;
+              if (g.accumulate) store_dw<float, true>(blk, p, g.k, NF - fw, nv - c, lane);
+              else store_dw<float, false>(blk, p, g.k, NF - fw, nv - c, lane);
+            } else {
+              __nv_bfloat16* p = static_cast<__nv_bfloat16*>(g.out) + o;
+              if (g.accumulate) store_dw<__nv_bfloat16, true>(blk, p, g.k, NF - fw, nv - c, lane);
+              else store_dw<__nv_bfloat16, false>(blk, p, g.k, NF - fw, nv - c, lane);
             }
           } else {
             // lane = feature, 32 rows: through shared memory to 64-byte
             // pieces of the rows
             __nv_bfloat16* blk = reinterpret_cast<__nv_bfloat16*>(stg);
-            __syncwarp();
 #pragma unroll
             for (int j = 0; j < 32; ++j) blk[j * 32 + lane] = __float2bfloat16_rn(__uint_as_float(r[j]));
             __syncwarp();
@@ -671,12 +718,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         if (!zero) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(free_bar[hb & 1]);
+          if (lane == 0) arrive_read(free_bar[hb & 1]);
           ++hb;
         }
       }
     }
-    if (MODE == GMM_DW && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
 
   tc_fence_before();
@@ -743,21 +789,6 @@ bool map_chunks(CUtensorMap* m, const void* p, int64_t E, int64_t rows, int64_t 
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// dw [E, n, k] in boxes of 128 bytes x 32 outputs, for stores.
-bool map_out(CUtensorMap* m, const void* p, int E, int n, int k, bool f32) {
-  auto fn = tc::encode_fn();
-  if (!fn) return false;
-  const cuuint64_t el = f32 ? 4 : 2;
-  cuuint64_t dims[3] = {(cuuint64_t)k, (cuuint64_t)n, (cuuint64_t)E};
-  cuuint64_t strides[2] = {k * el, (cuuint64_t)n * k * el};
-  cuuint32_t box[3] = {(cuuint32_t)(128 / el), 32, 1};
-  cuuint32_t es[3] = {1, 1, 1};
-  return fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
-            const_cast<void*>(p), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int MODE>
 cudaError_t launch(const GmmArgs& a, void* maps, int num_sms, cudaStream_t st) {
   using C = Cfg<MODE>;
@@ -776,7 +807,6 @@ cudaError_t launch(const GmmArgs& a, void* maps, int num_sms, cudaStream_t st) {
       if (e != cudaSuccess) return e;
     }
     g.maps = static_cast<const CUtensorMap*>(maps);
-    if (!map_out(&g.tmO, a.out, a.E, a.n, a.k, a.out_f32)) return cudaErrorInvalidValue;
   } else {
     if (a.rows == 0) return cudaSuccess;
     g.wide = MODE == GMM_DX && a.k % 64 == 0;
