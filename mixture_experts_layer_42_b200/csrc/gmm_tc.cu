@@ -25,8 +25,8 @@
 // Per CTA, 352 threads: warp 0 the TMA producer, warp 1 of the pair's leader
 // the MMA issuer, warps 2-9 the epilogue (two warps on each 32 TMEM lanes, in
 // turn over the columns), warp 10 the scheduler, which works the tiles out
-// ahead of the others. Results leave through a warp's own shared memory, so
-// that a store instruction covers whole sectors of a few rows. Rows of a tile past its expert's
+// ahead of the others. Rows leave through a warp's own shared memory (the
+// accumulator holds features by rows), dw straight from registers. Rows of a tile past its expert's
 // end are other rows of the matrix (their columns are not stored); only DW,
 // which sums over rows, reads through per-expert maps that end at the
 // expert's last row. Every wait is bounded (1 s); on expiry the kernel raises
@@ -56,10 +56,9 @@ constexpr int HEAVY = 256;                // rows above which an expert's tiles 
 
 template <int MODE> struct Cfg {
   static constexpr int HALVES = MODE == GMM_DW ? 1 : 2;
-  static constexpr int RING = MODE == GMM_DW ? 5 * 2 * TILE : 192 * 1024;
-  // staging of an epilogue warp: DW 32 outputs x 32 inputs in fp32, else 32
-  // rows x 32 features in bf16
-  static constexpr int STG = MODE == GMM_DW ? 4096 : 2048;
+  static constexpr int RING = MODE == GMM_DW ? 6 * 2 * TILE : 192 * 1024;
+  // staging of an epilogue warp: 32 rows x 32 features in bf16
+  static constexpr int STG = MODE == GMM_DW ? 0 : 2048;
   // experts' first rows and counts, and (FWD, DX) the tile prefixes of the
   // heavy and of the light ones
   static constexpr int TABLE = (MODE == GMM_DW ? 2 : 4) * (MAX_E + 1) * 4;
@@ -323,35 +322,81 @@ __device__ __forceinline__ void arrive_read(uint32_t remote_bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote_bar) : "memory");
 }
 
-// A warp's 32 x 32 block of dw from its staging (fp32, 16-byte places swizzled
-// by row), row and column bounds nr and nc: whole 128-byte rows of fp32 or 64
-// bytes of bf16 per store, added to what is there in fp32 when ACC.
-template <typename T, bool ACC>
-__device__ __forceinline__ void store_dw(const float4* stg, T* out, int64_t ld, int nr, int nc, int lane) {
-  constexpr int V = sizeof(T) == 4 ? 1 : 2;    // float4s a lane takes
-  constexpr int LPR = 8 / V, RPI = 32 / LPR;   // lanes per row, rows per instruction
-  const int c = lane % LPR * V;
+// 16 TMEM lanes x 32 columns: thread T gets of lanes T / 4 (r[4i], r[4i + 1])
+// and T / 4 + 8 (r[4i + 2], r[4i + 3]) the columns 8i + 2 (T % 4) and the next.
+__device__ __forceinline__ void tmem_ld16x32(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+// 32 outputs x 32 inputs of dw from a warp's registers (tmem_ld16x32 of its
+// lanes 0-15 and 16-31), nr and nc of them valid, added to what is there in
+// fp32 when `acc`. Four threads hold 8 neighbouring inputs of a row: 32 bytes
+// of fp32; for bf16 two blocks of 8 are exchanged between them, so that four
+// threads write 32 bytes of bf16 too (16-byte pieces of L2's sectors cost the
+// softmax layer's gradient a tenth).
+__device__ __forceinline__ void store_dw(const uint32_t (&r)[2][16], float* out, int64_t ld, int nr, int nc,
+                                         bool acc, int lane) {
 #pragma unroll
-  for (int it = 0; it < 32 / RPI; ++it) {
-    const int r = it * RPI + lane / LPR;
-    if (r >= nr || c * 4 >= nc) continue;
-    float f[4 * V];
+  for (int h = 0; h < 4; ++h) {
+    const int row = h * 8 + (lane >> 2);
+    float* p = out + (int64_t)row * ld + (lane & 3) * 2;
+    if (row < nr)
 #pragma unroll
-    for (int u = 0; u < V; ++u) {
-      const float4 v = stg[r * 8 + ((c + u) ^ (r & 7))];
-      f[4 * u] = v.x; f[4 * u + 1] = v.y; f[4 * u + 2] = v.z; f[4 * u + 3] = v.w;
+      for (int i = 0; i < 4; ++i)
+        if (8 * i < nc) {
+          float2 v = make_float2(__uint_as_float(r[h >> 1][4 * i + (h & 1) * 2]),
+                                 __uint_as_float(r[h >> 1][4 * i + (h & 1) * 2 + 1]));
+          if (acc) {
+            const float2 o = *reinterpret_cast<const float2*>(p + 8 * i);
+            v = make_float2(o.x + v.x, o.y + v.y);
+          }
+          *reinterpret_cast<float2*>(p + 8 * i) = v;
+        }
+  }
+}
+__device__ __forceinline__ void store_dw(const uint32_t (&r)[2][16], __nv_bfloat16* out, int64_t ld, int nr,
+                                         int nc, bool acc, int lane) {
+  const int t = lane & 3;
+#pragma unroll
+  for (int h = 0; h < 4; ++h) {
+    const int row = h * 8 + (lane >> 2);
+    // after the exchange threads 0 and 1 hold block 2u, threads 2 and 3 block
+    // 2u + 1: inputs 4 (t & 1) .. + 3
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      float v[2][2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float a = __uint_as_float(r[h >> 1][8 * u + (h & 1) * 2 + j]);
+        const float b = __uint_as_float(r[h >> 1][8 * u + 4 + (h & 1) * 2 + j]);
+        const float o = __shfl_xor_sync(0xffffffffu, (t & 2) ? a : b, 2);
+        // own and received pairs in order: inputs 2 (t & 1), and 4 + 2 (t & 1)
+        const float lo = (t & 2) ? o : a, hi = (t & 2) ? b : o;
+        const float x = __shfl_xor_sync(0xffffffffu, (t & 1) ? lo : hi, 1);
+        v[0][j] = (t & 1) ? x : lo;
+        v[1][j] = (t & 1) ? hi : x;
+      }
+      const int c = 16 * u + (t >> 1) * 8 + (t & 1) * 4;
+      if (row < nr && c < nc) {
+        __nv_bfloat162* p = reinterpret_cast<__nv_bfloat162*>(out + (int64_t)row * ld + c);
+        if (acc) {
+          const uint2 w = *reinterpret_cast<const uint2*>(p);
+          const float2 o0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w.x));
+          const float2 o1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w.y));
+          v[0][0] += o0.x; v[0][1] += o0.y; v[1][0] += o1.x; v[1][1] += o1.y;
+        }
+        const __nv_bfloat162 w0 = __floats2bfloat162_rn(v[0][0], v[0][1]);
+        const __nv_bfloat162 w1 = __floats2bfloat162_rn(v[1][0], v[1][1]);
+        *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&w0),
+                                                  *reinterpret_cast<const uint32_t*>(&w1));
+      }
     }
-    T* p = out + (int64_t)r * ld + c * 4;
-    Vec16<T> v;
-    if (ACC) {
-      float old[4 * V];
-      v.raw = *reinterpret_cast<const uint4*>(p);
-      v.to_float(old);
-#pragma unroll
-      for (int j = 0; j < 4 * V; ++j) f[j] += old[j];
-    }
-    v.from_float(f);
-    *reinterpret_cast<uint4*>(p) = v.raw;
   }
 }
 
@@ -669,37 +714,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         const int cb = t.c0 + h * t.nh;
 #pragma unroll 1
         for (int c = cg * 32; c < nv; c += 64) {
-          uint32_t r[32];
           __syncwarp();  // (the staging's last reads)
-          if (!zero) {
-            tmem_ld16(tb + c, *reinterpret_cast<uint32_t(*)[16]>(r));
-            tmem_ld16(tb + c + 16, *reinterpret_cast<uint32_t(*)[16]>(r + 16));
-            tmem_wait_ld();
-          } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) r[j] = 0;
-          }
           if (MODE == GMM_DW) {
-            // lane = output row of dw, 32 inputs
-            uint4* row = reinterpret_cast<uint4*>(stg + lane * 128);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              row[j ^ (lane & 7)] = make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
-            __syncwarp();
-            const float4* blk = reinterpret_cast<const float4*>(stg);
-            const int64_t o = ((int64_t)t.e * g.n + fw) * g.k + cb + c;
-            if (g.out_f32) {
-              float* p = static_cast<float*>(g.out) + o;
-              if (g.accumulate) store_dw<float, true>(blk, p, g.k, NF - fw, nv - c, lane);
-              else store_dw<float, false>(blk, p, g.k, NF - fw, nv - c, lane);
+            uint32_t r[2][16];
+            if (!zero) {
+              tmem_ld16x32(tb + c, r[0]);
+              tmem_ld16x32(tb + (16u << 16) + c, r[1]);
+              tmem_wait_ld();
             } else {
-              __nv_bfloat16* p = static_cast<__nv_bfloat16*>(g.out) + o;
-              if (g.accumulate) store_dw<__nv_bfloat16, true>(blk, p, g.k, NF - fw, nv - c, lane);
-              else store_dw<__nv_bfloat16, false>(blk, p, g.k, NF - fw, nv - c, lane);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) r[0][j] = r[1][j] = 0;
             }
+            const int64_t o = ((int64_t)t.e * g.n + fw) * g.k + cb + c;
+            if (g.out_f32)
+              store_dw(r, static_cast<float*>(g.out) + o, g.k, NF - fw, nv - c, g.accumulate, lane);
+            else
+              store_dw(r, static_cast<__nv_bfloat16*>(g.out) + o, g.k, NF - fw, nv - c, g.accumulate, lane);
           } else {
             // lane = feature, 32 rows: through shared memory to 64-byte
             // pieces of the rows
+            uint32_t r[32];
+            tmem_ld16(tb + c, *reinterpret_cast<uint32_t(*)[16]>(r));
+            tmem_ld16(tb + c + 16, *reinterpret_cast<uint32_t(*)[16]>(r + 16));
+            tmem_wait_ld();
             __nv_bfloat16* blk = reinterpret_cast<__nv_bfloat16*>(stg);
 #pragma unroll
             for (int j = 0; j < 32; ++j) blk[j * 32 + lane] = __float2bfloat16_rn(__uint_as_float(r[j]));
