@@ -38,7 +38,7 @@ __device__ __forceinline__ Span expert_span(const int32_t* offsets, int e, int64
 }
 
 // CUDA cores: fp32 and, as a cross-check of the tensor-core kernel, bf16.
-cudaError_t launch_gmm_simt(int mode, bool bf16, const GmmArgs& g, cudaStream_t st);
+cudaError_t launch_gmm_simt(int mode, bool bf16, const GmmArgs& g, int num_sms, cudaStream_t st);
 // Tensor cores: bf16. maps: 2 E TMA maps of workspace (DW).
 cudaError_t launch_gmm_tc(int mode, const GmmArgs& g, void* maps, int num_sms, cudaStream_t st);
 

@@ -71,7 +71,7 @@ moe_status run_gmm(int mode, const moe_grouped_shape* g, const void* a, const in
   if (bf16 && !simt_selected())
     return cuda_status(launch_gmm_tc(mode, p, at<void>(ws, grouped_layout(g->n_experts).maps),
                                      num_sms_current(), s));
-  return cuda_status(launch_gmm_simt(mode, bf16, p, s));
+  return cuda_status(launch_gmm_simt(mode, bf16, p, num_sms_current(), s));
 }
 
 bool w4_group_ok(int group) { return group == 32 || group == 64 || group == 128; }
