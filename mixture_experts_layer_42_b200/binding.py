@@ -10,6 +10,7 @@ Importing this module fails loudly when the library has not been built.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -298,19 +299,50 @@ def _need(ok: bool, what: str) -> None:
         raise ValueError(what)
 
 
-def _s_of(stream, t: torch.Tensor) -> ctypes.c_void_p:
-    """The given stream, or the current one of t's device."""
-    return _s(torch.cuda.current_stream(t.device) if stream is None and t.is_cuda else stream)
+def _args(stream, ws: torch.Tensor, *tensors) -> list:
+    """Device pointers of the (contiguous) tensors or None, then the workspace's
+    pointer and size and the stream: the given one, or the current one of the
+    workspace's device. All must live there."""
+    dev = ws.device
+    out = []
+    for t in tensors:
+        if t is None:
+            out.append(None)
+            continue
+        if t.device != dev:
+            raise ValueError("tensors on two devices")
+        if not t.is_contiguous():
+            raise ValueError("tensors passed to libmoe must be contiguous")
+        out.append(t.data_ptr())
+    if not ws.is_contiguous():
+        raise ValueError("tensors passed to libmoe must be contiguous")
+    out += [ws.data_ptr(), ws.numel() * ws.element_size(), _raw_stream(stream, dev)]
+    return out
+
+
+# The current stream's handle by device index, without a torch.cuda.Stream
+# around it (2 us a call, a fifth of a small call's host time).
+_current_raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _raw_stream(stream, device: torch.device):
+    if stream is not None:
+        return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+    return _current_raw(device.index) if device.type == "cuda" else None
+
+
+_DT = {torch.float32: MOE_DT_F32, torch.bfloat16: MOE_DT_BF16}
 
 
 def _dt(dtype: torch.dtype) -> int:
-    _need(dtype in (torch.float32, torch.bfloat16), f"libmoe runs float32 and bfloat16, not {dtype}")
-    return MOE_DT_F32 if dtype == torch.float32 else MOE_DT_BF16
+    _need(dtype in _DT, f"libmoe runs float32 and bfloat16, not {dtype}")
+    return _DT[dtype]
 
 
+@functools.lru_cache(maxsize=1024)
 def grouped_shape(rows: int, n_experts: int, n: int, k: int, dtype: torch.dtype) -> moe_grouped_shape:
-    return moe_grouped_shape(rows=int(rows), n_experts=int(n_experts), n=int(n), k=int(k),
-                             dtype=_dt(dtype))
+    return moe_grouped_shape(int(rows), int(n_experts), int(n), int(k), _dt(dtype))
 
 
 def moe_grouped_workspace_size(rows: int, n_experts: int, n: int, k: int, dtype: torch.dtype) -> int:
@@ -330,45 +362,43 @@ def alloc_workspace_grouped(rows: int, n_experts: int, n: int, k: int, dtype=tor
     return ws
 
 
-def _grouped(rows_x, rows_y, w, offsets, extra=()):
+def _grouped(x, y, w, offsets) -> moe_grouped_shape:
     """The shape of a grouped product from its row matrices x [R, K] and
-    y [R, N] (either may be None) and the stacked weights [E, N, K]."""
-    _need(w.dim() == 3, "the experts' matrices must be one [E, N, K] tensor")
+    y [R, N] and the stacked weights [E, N, K]."""
+    if w.dim() != 3:
+        raise ValueError("the experts' matrices must be one [E, N, K] tensor")
     E, n, k = w.shape
-    R = (rows_x if rows_x is not None else rows_y).shape[0]
-    for t, cols, name in ((rows_x, k, "[R, K]"), (rows_y, n, "[R, N]")):
-        _need(t is None or tuple(t.shape) == (R, cols), f"row matrix is not {name} of the weights' shape")
-    act = (rows_x if rows_x is not None else rows_y).dtype
-    _need(all(t is None or t.dtype == act for t in (rows_x, rows_y)), "row matrices of two types")
-    _need(offsets.dtype == torch.int32 and offsets.numel() == E + 1, "offsets must be int32 [E + 1]")
-    for t in (rows_x, rows_y, offsets) + tuple(extra):
-        _need(t is None or t.device == w.device, "tensors on two devices")
-    return grouped_shape(R, E, n, k, act)
+    R = x.shape[0]
+    if x.shape != (R, k) or y.shape != (R, n):
+        raise ValueError("the row matrices are not [R, K] and [R, N] of the weights' shape")
+    if x.dtype != y.dtype:
+        raise ValueError("row matrices of two types")
+    if offsets.dtype != torch.int32 or offsets.numel() != E + 1:
+        raise ValueError("offsets must be int32 [E + 1]")
+    return grouped_shape(R, E, n, k, x.dtype)
 
 
 def moe_grouped_matmul(x, offsets, w, y, ws, stream=None) -> None:
     """y[r] = w[e] x[r] for the rows r of expert e: x [R, K], w [E, N, K], y [R, N]."""
-    g = _grouped(x, y, w, offsets, (ws,))
+    g = _grouped(x, y, w, offsets)
     _need(w.dtype == x.dtype, "weights and rows of two types")
-    _check(_lib.moe_grouped_matmul(ctypes.byref(g), _p(x), _p(offsets), _p(w), _p(y), _p(ws),
-                                   ws.numel(), _s_of(stream, ws)), "moe_grouped_matmul")
+    _check(_lib.moe_grouped_matmul(g, *_args(stream, ws, x, offsets, w, y)), "moe_grouped_matmul")
 
 
 def moe_grouped_matmul_dx(dy, offsets, w, dx, ws, stream=None) -> None:
     """dx[r] = w[e]^T dy[r]: dy [R, N], w [E, N, K], dx [R, K]."""
-    g = _grouped(dx, dy, w, offsets, (ws,))
+    g = _grouped(dx, dy, w, offsets)
     _need(w.dtype == dy.dtype, "weights and rows of two types")
-    _check(_lib.moe_grouped_matmul_dx(ctypes.byref(g), _p(dy), _p(offsets), _p(w), _p(dx), _p(ws),
-                                      ws.numel(), _s_of(stream, ws)), "moe_grouped_matmul_dx")
+    _check(_lib.moe_grouped_matmul_dx(g, *_args(stream, ws, dy, offsets, w, dx)), "moe_grouped_matmul_dx")
 
 
 def moe_grouped_matmul_dw(dy, x, offsets, dw, ws, accumulate=False, stream=None) -> None:
     """dw[e] (+)= sum of dy[r] x[r]^T over e's rows: dy [R, N], x [R, K],
     dw [E, N, K] in x's type or fp32."""
-    g = _grouped(x, dy, dw, offsets, (ws,))
-    _check(_lib.moe_grouped_matmul_dw(ctypes.byref(g), _p(dy), _p(x), _p(offsets), _dt(dw.dtype),
-                                      1 if accumulate else 0, _p(dw), _p(ws), ws.numel(),
-                                      _s_of(stream, ws)), "moe_grouped_matmul_dw")
+    g = _grouped(x, dy, dw, offsets)
+    dyp, xp, op, dwp, *rest = _args(stream, ws, dy, x, offsets, dw)
+    _check(_lib.moe_grouped_matmul_dw(g, dyp, xp, op, _dt(dw.dtype), 1 if accumulate else 0, dwp, *rest),
+           "moe_grouped_matmul_dw")
 
 
 def moe_quantize_w4(w, group, q, scales, stream=None) -> None:
@@ -378,50 +408,52 @@ def moe_quantize_w4(w, group, q, scales, stream=None) -> None:
     _need(q.dtype == torch.uint8 and 2 * q.numel() == w.numel(), "codes must be uint8 [E, N, K / 2]")
     _need(scales.dtype == torch.bfloat16 and scales.numel() * int(group) == w.numel(),
           "scales must be bfloat16 [E, K / group, N]")
-    g = grouped_shape(0, E, n, k, w.dtype)
-    _check(_lib.moe_quantize_w4(ctypes.byref(g), int(group), _p(w), _p(q), _p(scales),
-                                _s_of(stream, w)), "moe_quantize_w4")
+    qp, sp, wp, _, st = _args(stream, w, q, scales)
+    _check(_lib.moe_quantize_w4(grouped_shape(0, E, n, k, w.dtype), int(group), wp, qp, sp, st),
+           "moe_quantize_w4")
 
 
-def _w4_shape(x, src, offsets, out, mats, ws):
+def _w4_shape(x, src, offsets, out, q, s):
     """Shape and group of a 4-bit product from its codes q [E, N, K / 2] and
     scales [E, K / group, N]."""
-    q, s = mats[0]
-    _need(q.dim() == 3 and s.dim() == 3, "codes [E, N, K / 2] and scales [E, K / group, N] expected")
+    if q.dim() != 3 or s.dim() != 3 or q.dtype != torch.uint8 or s.dtype != torch.bfloat16:
+        raise ValueError("codes uint8 [E, N, K / 2] and scales bfloat16 [E, K / group, N] expected")
     E, n, k = q.shape[0], q.shape[1], 2 * q.shape[2]
-    _need(s.shape[1] > 0 and k % s.shape[1] == 0, "scales do not divide the inputs into groups")
-    for qq, ss in mats:
-        _need(qq.dtype == torch.uint8 and tuple(qq.shape) == (E, n, k // 2), "codes must be uint8 [E, N, K / 2]")
-        _need(ss.dtype == torch.bfloat16 and tuple(ss.shape) == (E, s.shape[1], n),
-              "scales must be bfloat16 [E, K / group, N]")
+    groups = s.shape[1]
+    if s.shape != (E, groups, n) or groups < 1 or k % groups:
+        raise ValueError("scales must be bfloat16 [E, K / group, N]")
     R = out.shape[0]
-    _need(x.dim() == 2 and x.shape[1] == k and tuple(out.shape) == (R, n), "x [rows, K] and out [R, N] expected")
-    _need(out.dtype == x.dtype, "rows and outputs of two types")
-    _need(src is None or (src.dtype == torch.int32 and src.numel() >= R), "src must be int32 [R]")
-    _need(offsets.dtype == torch.int32 and offsets.numel() == E + 1, "offsets must be int32 [E + 1]")
-    for t in (x, src, offsets, out, ws) + tuple(t for m in mats for t in m):
-        _need(t is None or t.device == q.device, "tensors on two devices")
-    return grouped_shape(R, E, n, k, x.dtype), k // s.shape[1]
+    if x.dim() != 2 or x.shape[1] != k or out.shape != (R, n):
+        raise ValueError("x [rows, K] and out [R, N] expected")
+    if out.dtype != x.dtype:
+        raise ValueError("rows and outputs of two types")
+    if src is not None and (src.dtype != torch.int32 or src.numel() < R):
+        raise ValueError("src must be int32 [R]")
+    if offsets.dtype != torch.int32 or offsets.numel() != E + 1:
+        raise ValueError("offsets must be int32 [E + 1]")
+    return grouped_shape(R, E, n, k, x.dtype), k // groups
 
 
 def _w4m(q=None, scales=None) -> moe_w4_matrix:
-    return moe_w4_matrix(None if q is None else _p(q), None if scales is None else _p(scales))
+    return moe_w4_matrix(None if q is None else q.data_ptr(), None if scales is None else scales.data_ptr())
 
 
 def moe_grouped_matvec_w4(x, src, offsets, q, scales, y, ws, stream=None) -> None:
     """y[r] = W_e x[src[r]] (x[r] when src is None), W_e in 4 bits."""
-    g, group = _w4_shape(x, src, offsets, y, ((q, scales),), ws)
-    _check(_lib.moe_grouped_matvec_w4(ctypes.byref(g), group, x.shape[0], _p(x), _p(src), _p(offsets),
-                                      ctypes.byref(_w4m(q, scales)), _p(y), _p(ws), ws.numel(),
-                                      _s_of(stream, ws)), "moe_grouped_matvec_w4")
+    g, group = _w4_shape(x, src, offsets, y, q, scales)
+    xp, srcp, op, qp, sp, yp, *rest = _args(stream, ws, x, src, offsets, q, scales, y)
+    _check(_lib.moe_grouped_matvec_w4(g, group, x.shape[0], xp, srcp, op, moe_w4_matrix(qp, sp), yp, *rest),
+           "moe_grouped_matvec_w4")
 
 
 def moe_grouped_swiglu_w4(x, src, offsets, q1, s1, q3, s3, h, ws, stream=None) -> None:
     """h[r] = silu(W1_e x[src[r]]) * (W3_e x[src[r]]) (x[r] when src is None)."""
-    g, group = _w4_shape(x, src, offsets, h, ((q1, s1), (q3, s3)), ws)
-    _check(_lib.moe_grouped_swiglu_w4(ctypes.byref(g), group, x.shape[0], _p(x), _p(src), _p(offsets),
-                                      ctypes.byref(_w4m(q1, s1)), ctypes.byref(_w4m(q3, s3)), _p(h),
-                                      _p(ws), ws.numel(), _s_of(stream, ws)), "moe_grouped_swiglu_w4")
+    g, group = _w4_shape(x, src, offsets, h, q1, s1)
+    if q3.shape != q1.shape or s3.shape != s1.shape or q3.dtype != q1.dtype or s3.dtype != s1.dtype:
+        raise ValueError("the codes and scales of w1 and w3 differ in shape or type")
+    xp, srcp, op, q1p, s1p, q3p, s3p, hp, *rest = _args(stream, ws, x, src, offsets, q1, s1, q3, s3, h)
+    _check(_lib.moe_grouped_swiglu_w4(g, group, x.shape[0], xp, srcp, op, moe_w4_matrix(q1p, s1p),
+                                      moe_w4_matrix(q3p, s3p), hp, *rest), "moe_grouped_swiglu_w4")
 
 
 def moe_workspace_size_w4(cfg, T: int) -> int:
@@ -439,15 +471,16 @@ def alloc_workspace_w4(cfg, T: int, device="cuda") -> torch.Tensor:
 def w4_weights(group, w1, w3, w2, ws1=None, ws3=None, ws2=None) -> moe_w4_weights:
     """The C struct of 4-bit expert weights; each matrix is a pair (codes,
     scales) of device tensors, kept alive by the caller."""
+    for m in (w1, w3, w2, ws1, ws3, ws2):
+        _need(m is None or all(t.is_contiguous() for t in m), "tensors passed to libmoe must be contiguous")
     return moe_w4_weights(*[_w4m(*(m or (None, None))) for m in (w1, w3, w2, ws1, ws3, ws2)],
                           int(group))
 
 
 def moe_forward_w4(cfg, x, w_router, bias, w4: moe_w4_weights, y, ws, weights_out=None, idx_out=None,
                    stream=None) -> None:
-    _check(_lib.moe_forward_w4(_c(cfg), x.shape[0], _p(x), _p(w_router), _p(bias), ctypes.byref(w4),
-                               _p(y), _p(weights_out), _p(idx_out), _p(ws), ws.numel(),
-                               _s_of(stream, ws)), "moe_forward_w4")
+    xp, rp, bp, yp, wp, ip, *rest = _args(stream, ws, x, w_router, bias, y, weights_out, idx_out)
+    _check(_lib.moe_forward_w4(_c(cfg), x.shape[0], xp, rp, bp, w4, yp, wp, ip, *rest), "moe_forward_w4")
 
 
 def moe_check_error(ws, stream=None) -> int:

@@ -1,6 +1,8 @@
 // Host helpers shared by the C ABI's entry points.
 #pragma once
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace moe {
@@ -20,6 +22,20 @@ moe_status bind_device(cudaStream_t s, const void* ptr);
 
 // SMs of the current device.
 int num_sms_current();
+
+// Let `kernel` use `bytes` of dynamic shared memory on the current device:
+// asked of the runtime once per kernel and device (`done`: the kernel's own).
+template <typename K>
+cudaError_t allow_smem(K kernel, int bytes, std::atomic<uint64_t>* done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done->load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done->fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 // Whether moe_select_expert_kernel chose the CUDA-core kernels.
 bool simt_selected();

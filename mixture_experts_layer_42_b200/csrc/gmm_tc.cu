@@ -31,6 +31,7 @@
 // which sums over rows, reads through per-expert maps that end at the
 // expert's last row. Every wait is bounded (1 s); on expiry the kernel raises
 // the error word's timeout bit, drains its copies and returns.
+#include "api_common.cuh"
 #include "gmm.cuh"
 #include "tc_common.cuh"
 
@@ -869,8 +870,8 @@ cudaError_t launch(const GmmArgs& a, void* maps, int num_sms, cudaStream_t st) {
   const int64_t nf = ceil_div(MODE == GMM_DX ? a.k : a.n, 2 * FM);
   const int64_t bound = MODE == GMM_DW ? nf * ceil_div(a.k, MAXN) * a.E : nf * (a.rows / 32 + a.E);
   const int pairs = (int)(bound < num_sms / 2 ? bound : num_sms / 2);
-  cudaError_t e = cudaFuncSetAttribute(gmm_tc_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)C::SMEM);
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem(gmm_tc_kernel<MODE>, (int)C::SMEM, &allowed);
   if (e != cudaSuccess) return e;
   gmm_tc_kernel<MODE><<<2 * pairs, NUM_THREADS, C::SMEM, st>>>(g);
   return cudaGetLastError();

@@ -3,6 +3,8 @@
 // input in the low half; w[i][j] = (code - 8) * scale[j / group][i].
 #include "w4.cuh"
 
+#include "api_common.cuh"
+
 #include <cstring>
 
 #include "tc_common.cuh"
@@ -482,8 +484,8 @@ bool map_scales(CUtensorMap* m, const void* p, int64_t E, int64_t groups, int64_
 template <bool SWIGLU, int NT, int GPC>
 cudaError_t launch_w4_kernel(const W4Args& g, const W4Tma& m, int64_t bound, int num_sms, cudaStream_t st) {
   using C = W4Cfg<NT, GPC == 1>;
-  cudaError_t e = cudaFuncSetAttribute(w4_kernel<SWIGLU, NT, GPC>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem(w4_kernel<SWIGLU, NT, GPC>, (int)C::SMEM, &allowed);
   if (e != cudaSuccess) return e;
   const int64_t most = (int64_t)C::CTAS * num_sms;
   w4_kernel<SWIGLU, NT, GPC><<<(unsigned)(bound < most ? bound : most), NUM_THREADS, C::SMEM, st>>>(g, m);
