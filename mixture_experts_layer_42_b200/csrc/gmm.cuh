@@ -22,6 +22,15 @@ struct GmmArgs {
   uint32_t* err;
 };
 
+// Every kernel of these calls is launched as a programmatic dependent of what
+// is before it in the stream: it may start (its launch, barriers and other
+// set-up overlap that kernel's end), lets the next one start, and waits for the
+// grids before it to complete before it reads or writes any tensor.
+__device__ __forceinline__ void grid_dependency() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // Expert e's rows [b, b + count), or none when its offsets are not
 // 0 <= offsets[e] <= offsets[e + 1] <= rows (`bad` then says so).
 struct Span {

@@ -166,6 +166,7 @@ __global__ void __launch_bounds__(GTHREADS, C::CTAS) gmm_simt_kernel(const GmmAr
   using SB = Slice<T, MODE == GMM_FWD, GN, GK>;
   __shared__ __align__(16) float As[2][GK][SA::LD];
   __shared__ __align__(16) float Bs[2][GK][SB::LD];
+  grid_dependency();
   const int tid = threadIdx.x;
   const int NJ = MODE == GMM_FWD ? g.n : g.k;
   const int nj = ceil_div(NJ, GN);  // column tiles, fastest over the CTAs
@@ -275,9 +276,9 @@ cudaError_t launch(const GmmArgs& g, int num_sms, cudaStream_t st) {
   const int64_t ctas = small ? ctas_of<Small>(MODE, g) : ctas_of<Large>(MODE, g);
   if (ctas == 0) return cudaSuccess;
   if (ctas > INT32_MAX) return cudaErrorInvalidValue;
-  if (small) gmm_simt_kernel<T, TO, MODE, Small><<<(unsigned)ctas, GTHREADS, 0, st>>>(g);
-  else gmm_simt_kernel<T, TO, MODE, Large><<<(unsigned)ctas, GTHREADS, 0, st>>>(g);
-  return cudaGetLastError();
+  const dim3 grid((unsigned)ctas), block(GTHREADS);
+  return small ? launch_pdl(true, gmm_simt_kernel<T, TO, MODE, Small>, grid, block, 0, st, g)
+               : launch_pdl(true, gmm_simt_kernel<T, TO, MODE, Large>, grid, block, 0, st, g);
 }
 
 template <typename T>

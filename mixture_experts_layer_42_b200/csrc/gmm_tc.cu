@@ -444,6 +444,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
+    grid_dependency();
     const int per = (E + 31) / 32;
     bool bad = false;
     int maxc = 0;
@@ -519,6 +520,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if (warp > 0) grid_dependency();
   cluster_sync();  // barriers of both CTAs initialised before any cross-CTA use
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
@@ -783,6 +785,7 @@ struct EndMapArgs {
 __global__ void __launch_bounds__(256) gmm_end_maps_kernel(const __grid_constant__ EndMapArgs a,
                                                            const int32_t* offsets, int64_t rows, int E) {
   __shared__ __align__(128) CUtensorMap sm[8];
+  grid_dependency();
   const int w = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int e = blockIdx.x * 8 + w;
   if (e >= E) return;  // whole warps
@@ -840,8 +843,8 @@ cudaError_t launch(const GmmArgs& a, void* maps, int num_sms, cudaStream_t st) {
       if (!(g.wide ? map_chunks(&m.base[0], a.a, 1, a.rows, a.n) : map_rows(&m.base[0], a.a, a.rows, a.n, BK)) ||
           !map_rows(&m.base[1], a.b, a.rows, a.k, BK))
         return cudaErrorInvalidValue;
-      gmm_end_maps_kernel<<<dim3((unsigned)ceil_div(a.E, 8), 2), 256, 0, st>>>(m, a.offsets, a.rows, a.E);
-      const cudaError_t e = cudaGetLastError();
+      const cudaError_t e = launch_pdl(true, gmm_end_maps_kernel, dim3((unsigned)ceil_div(a.E, 8), 2), dim3(256),
+                                       0, st, m, a.offsets, a.rows, a.E);
       if (e != cudaSuccess) return e;
     }
     g.maps = static_cast<const CUtensorMap*>(maps);
@@ -873,8 +876,7 @@ cudaError_t launch(const GmmArgs& a, void* maps, int num_sms, cudaStream_t st) {
   static std::atomic<uint64_t> allowed{0};
   cudaError_t e = allow_smem(gmm_tc_kernel<MODE>, (int)C::SMEM, &allowed);
   if (e != cudaSuccess) return e;
-  gmm_tc_kernel<MODE><<<2 * pairs, NUM_THREADS, C::SMEM, st>>>(g);
-  return cudaGetLastError();
+  return launch_pdl(true, gmm_tc_kernel<MODE>, dim3(2 * pairs), dim3(NUM_THREADS), C::SMEM, st, g);
 }
 
 }  // namespace

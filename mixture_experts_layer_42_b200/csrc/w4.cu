@@ -23,6 +23,7 @@ template <typename T>
 __global__ void __launch_bounds__(256) quantize_w4_kernel(const T* w, int64_t rows, int n, int k,
                                                           int group, uint8_t* q,
                                                           __nv_bfloat16* scales) {
+  grid_dependency();
   const int kc = ceil_div(k, 256);
   const int64_t unit = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
   if (unit >= rows * kc) return;
@@ -240,6 +241,7 @@ __global__ void __launch_bounds__(NUM_THREADS, W4Cfg<NT, GPC == 1>::CTAS)
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
   __syncthreads();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 
   if (warp == 0) {
     // ---------------------------------------------------------------- TMA producer
@@ -361,6 +363,11 @@ __global__ void __launch_bounds__(NUM_THREADS, W4Cfg<NT, GPC == 1>::CTAS)
       }
       if (end) break;
     }
+    // The next kernel may start once every CTA has asked for its last copies;
+    // any earlier, and CTAs of a next call of this kernel would fill the SMs
+    // unevenly while this one's still run (one token's up-projection: 50
+    // instead of 39 us a call).
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (!ok && lane == 0)
       for (int j = 0; j < STAGES; ++j) {
         const int n = issued / STAGES + (j < issued % STAGES ? 1 : 0);
@@ -445,13 +452,12 @@ cudaError_t launch_quantize_w4(bool bf16, const void* w, int64_t E, int n, int k
   const int64_t rows = E * n, units = rows * ceil_div(k, 256);
   const int64_t ctas = ceil_div<int64_t>(units, 8);
   if (ctas > INT32_MAX) return cudaErrorInvalidValue;
+  const dim3 grid((unsigned)ctas), block(256);
   if (bf16)
-    quantize_w4_kernel<<<(unsigned)ctas, 256, 0, st>>>(static_cast<const __nv_bfloat16*>(w), rows, n,
-                                                       k, group, q, scales);
-  else
-    quantize_w4_kernel<<<(unsigned)ctas, 256, 0, st>>>(static_cast<const float*>(w), rows, n, k,
-                                                       group, q, scales);
-  return cudaGetLastError();
+    return launch_pdl(true, quantize_w4_kernel<__nv_bfloat16>, grid, block, 0, st,
+                      static_cast<const __nv_bfloat16*>(w), rows, n, k, group, q, scales);
+  return launch_pdl(true, quantize_w4_kernel<float>, grid, block, 0, st, static_cast<const float*>(w), rows, n,
+                    k, group, q, scales);
 }
 
 namespace {
@@ -488,8 +494,8 @@ cudaError_t launch_w4_kernel(const W4Args& g, const W4Tma& m, int64_t bound, int
   cudaError_t e = allow_smem(w4_kernel<SWIGLU, NT, GPC>, (int)C::SMEM, &allowed);
   if (e != cudaSuccess) return e;
   const int64_t most = (int64_t)C::CTAS * num_sms;
-  w4_kernel<SWIGLU, NT, GPC><<<(unsigned)(bound < most ? bound : most), NUM_THREADS, C::SMEM, st>>>(g, m);
-  return cudaGetLastError();
+  return launch_pdl(true, w4_kernel<SWIGLU, NT, GPC>, dim3((unsigned)(bound < most ? bound : most)),
+                    dim3(NUM_THREADS), C::SMEM, st, g, m);
 }
 
 template <bool SWIGLU, int NT>
