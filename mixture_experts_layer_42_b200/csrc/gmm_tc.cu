@@ -518,6 +518,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
                  "r"(TMEM_COLS));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
   }
+  if (MODE != GMM_DW) {
+    // zeros for the columns that no box brings (see row_box)
+    for (uint32_t i = threadIdx.x; i < C::RING / 16; i += NUM_THREADS)
+      reinterpret_cast<uint4*>(tiles)[i] = make_uint4(0, 0, 0, 0);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
   tc_fence_before();
   __syncthreads();
   if (warp > 0) grid_dependency();
