@@ -95,6 +95,7 @@ __device__ __forceinline__ bool find_tile(const GmmArgs& g, int mi, int* e_out, 
   if (tid == 0) s_e = -1;
   int lsum = 0;
   bool bad = false;
+#pragma unroll 4
   for (int u = 0; u < per; ++u) {
     const int x = tid * per + u;
     if (x < g.E) {

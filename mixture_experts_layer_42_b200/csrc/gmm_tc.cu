@@ -444,74 +444,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
-    grid_dependency();
-    const int per = (E + 31) / 32;
-    bool bad = false;
-    int maxc = 0;
-    int64_t rows = 0;
-    int tl[5] = {0, 0, 0, 0, 0};  // tiles at a cap of 512, 256, 128, 64, 32 rows
-    for (int u = 0; u < per; ++u) {
-      const int e = lane * per + u;
-      if (e < E) {
-        const Span s = expert_span(g.offsets, e, g.rows);
-        bad |= s.bad;
-        cnt[e] = s.count;
-        off[e] = s.b;
-        maxc = max(maxc, s.count);
-        rows += s.count;
-#pragma unroll
-        for (int c = 0; c < 5; ++c) tl[c] += (int)(((int64_t)s.count + (512 >> c) - 1) >> (9 - c));
-      }
-    }
-    if (bad && blockIdx.x == 0) set_error(g.err, ERRBIT_BAD_INDEX);
-    if (MODE != GMM_DW) {
-      // The rows a tile may hold. What bounds large calls is the traffic from
-      // L2, 256 + rows per tile and 64 of the reduction, shared by the pairs;
-      // a small call also waits for its last tile, up to 256 + cap.
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        maxc = max(maxc, __shfl_xor_sync(0xffffffffu, maxc, o));
-        rows += __shfl_xor_sync(0xffffffffu, rows, o);
-#pragma unroll
-        for (int c = 0; c < 5; ++c) tl[c] += __shfl_xor_sync(0xffffffffu, tl[c], o);
-      }
-      int cap = 512;
-      int64_t best = INT64_MAX;
-#pragma unroll
-      for (int c = 0; c < 5; ++c) {
-        const int most = 256 + min(512 >> c, round32(maxc));
-        const int64_t all = ((int64_t)tl[c] * 256 + rows) * nf / npairs;
-        const int64_t cost = tl[c] * (int64_t)nf <= npairs ? most : all + most;
-        if (cost < best) { best = cost; cap = 512 >> c; }
-      }
-      int sum[2] = {0, 0};  // token tiles of this lane's light and heavy experts
-      for (int u = 0; u < per; ++u) {
-        const int e = lane * per + u;
-        if (e < E) sum[cnt[e] > HEAVY] += (int)(((int64_t)cnt[e] + cap - 1) / cap);
-      }
-      int run[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        int incl = sum[h];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int p = __shfl_up_sync(0xffffffffu, incl, o);
-          if (lane >= o) incl += p;
-        }
-        run[h] = incl - sum[h];
-        if (lane == 31) (h ? PH : PL)[E] = incl;
-      }
-      for (int u = 0; u < per; ++u) {
-        const int e = lane * per + u;
-        if (e < E) {
-          PL[e] = run[0];
-          PH[e] = run[1];
-          const int mt = (int)(((int64_t)cnt[e] + cap - 1) / cap);
-          if (cnt[e] > HEAVY) run[1] += mt; else run[0] += mt;
-        }
-      }
-    }
-    __syncwarp();
   } else if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(tmem_slot)),
@@ -524,25 +456,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       reinterpret_cast<uint4*>(tiles)[i] = make_uint4(0, 0, 0, 0);
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
+  grid_dependency();
+  bool bad = false;
+#pragma unroll 4
+  for (int e = threadIdx.x; e < E; e += NUM_THREADS) {
+    const Span sp = expert_span(g.offsets, e, g.rows);
+    bad |= sp.bad;
+    cnt[e] = sp.count;
+    off[e] = sp.b;
+  }
+  if (bad && blockIdx.x == 0) set_error(g.err, ERRBIT_BAD_INDEX);
   tc_fence_before();
   __syncthreads();
-  if (warp > 0) grid_dependency();
   cluster_sync();  // barriers of both CTAs initialised before any cross-CTA use
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-
-  Sched S;
-  S.off = off;
-  S.cnt = cnt;
-  S.PH = PH;
-  S.PL = PL;
-  S.E = E;
-  S.nf = nf;
-  S.nc = (g.k + MAXN - 1) / MAXN;
-  S.n = g.n;
-  S.k = g.k;
-  S.heavy = MODE == GMM_DW ? 0 : nf * PH[E];
-  S.total = MODE == GMM_DW ? E * nf * S.nc : S.heavy + nf * PL[E];
 
   if (warp == 0) {
     // ---------------------------------------------------------------- TMA producer (both CTAs)
@@ -685,6 +613,79 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     }
   } else if (warp == 10) {
     // ---------------------------------------------------------------- scheduler (both CTAs)
+    if (MODE != GMM_DW) {
+      const int per = (E + 31) / 32;
+      int maxc = 0;
+      int64_t rows = 0;
+      int tl[5] = {0, 0, 0, 0, 0};  // tiles at a cap of 512, 256, 128, 64, 32 rows
+      for (int u = 0; u < per; ++u) {
+        const int e = lane * per + u;
+        if (e < E) {
+          maxc = max(maxc, cnt[e]);
+          rows += cnt[e];
+#pragma unroll
+          for (int c = 0; c < 5; ++c) tl[c] += (int)(((int64_t)cnt[e] + (512 >> c) - 1) >> (9 - c));
+        }
+      }
+      // The rows a tile may hold. What bounds large calls is the traffic from
+      // L2, 256 + rows per tile and 64 of the reduction, shared by the pairs;
+      // a small call also waits for its last tile, up to 256 + cap.
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        maxc = max(maxc, __shfl_xor_sync(0xffffffffu, maxc, o));
+        rows += __shfl_xor_sync(0xffffffffu, rows, o);
+#pragma unroll
+        for (int c = 0; c < 5; ++c) tl[c] += __shfl_xor_sync(0xffffffffu, tl[c], o);
+      }
+      int cap = 512;
+      int64_t best = INT64_MAX;
+#pragma unroll
+      for (int c = 0; c < 5; ++c) {
+        const int most = 256 + min(512 >> c, round32(maxc));
+        const int64_t all = ((int64_t)tl[c] * 256 + rows) * nf / npairs;
+        const int64_t cost = tl[c] * (int64_t)nf <= npairs ? most : all + most;
+        if (cost < best) { best = cost; cap = 512 >> c; }
+      }
+      int sum[2] = {0, 0};  // token tiles of this lane's light and heavy experts
+      for (int u = 0; u < per; ++u) {
+        const int e = lane * per + u;
+        if (e < E) sum[cnt[e] > HEAVY] += (int)(((int64_t)cnt[e] + cap - 1) / cap);
+      }
+      int run[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        int incl = sum[h];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int p = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += p;
+        }
+        run[h] = incl - sum[h];
+        if (lane == 31) (h ? PH : PL)[E] = incl;
+      }
+      for (int u = 0; u < per; ++u) {
+        const int e = lane * per + u;
+        if (e < E) {
+          PL[e] = run[0];
+          PH[e] = run[1];
+          const int mt = (int)(((int64_t)cnt[e] + cap - 1) / cap);
+          if (cnt[e] > HEAVY) run[1] += mt; else run[0] += mt;
+        }
+      }
+    }
+    __syncwarp();
+    Sched S;
+    S.off = off;
+    S.cnt = cnt;
+    S.PH = PH;
+    S.PL = PL;
+    S.E = E;
+    S.nf = nf;
+    S.nc = (g.k + MAXN - 1) / MAXN;
+    S.n = g.n;
+    S.k = g.k;
+    S.heavy = MODE == GMM_DW ? 0 : nf * PH[E];
+    S.total = MODE == GMM_DW ? E * nf * S.nc : S.heavy + nf * PL[E];
     uint32_t q = 0, ph = 0;
     for (int i = pair;; i += npairs) {
       Tile t;

@@ -7,7 +7,9 @@ groups err by at most 2^-23 of the partial sums each and a scale's product by
 2^-24, so (k + 4) 2^-23 S; the rounding to bf16 adds 2^-8 of the result. The
 SwiGLU form carries its two sums' errors through silu (slope at most 1.1), and
 the fast exponential errs by (2 + 1.2 |a|) 2^-22, so silu by 2^-21 (4 + |a|)
-of itself."""
+of itself. With few rows per expert the sums within a group are exact integers
+of x's 30-bit digits, which rounds inputs below 2^-22 of the largest of their
+128 by at most 2^-31 of it: less than one of the k + 4 roundings above."""
 
 import numpy as np
 import pytest
@@ -21,6 +23,11 @@ from tests.gpu_util import Layer, check_routing, check_y, host, to_np
 pytestmark = pytest.mark.gpu
 
 BF = torch.bfloat16
+
+# The digits' unit is 2^(E - 29) with E at least -97: an input is off by at most
+# half of 2^-126 (fp32's smallest normal number), whatever its size; a result
+# below bf16's smallest normal number by half of its step there, 2^-134.
+TINY = 2.0 ** -127
 
 
 def quantize(w, group):
@@ -106,15 +113,16 @@ class Problem:
                 ok = (self.src[r] >= 0) & (self.src[r] < self.x.shape[0])
                 x = self.x[self.src[r].clamp(0, self.x.shape[0] - 1).long()].double() * ok[:, None]
             a, S = x @ w[0][e].T, x.abs() @ w[0][e].abs().T
-            da = (self.k + 4) * 2.0 ** -23 * S
+            da = (self.k + 4) * 2.0 ** -23 * S + TINY * w[0][e].abs().sum(1)
             ref, tol = a, da
             if len(w) == 2:
                 b, Sb = x @ w[1][e].T, x.abs() @ w[1][e].abs().T
                 sl = a * torch.sigmoid(a)
                 ref = sl * b
-                tol = 1.1 * da * (b.abs() + da) + sl.abs() * (self.k + 4) * 2.0 ** -23 * Sb \
+                db = (self.k + 4) * 2.0 ** -23 * Sb + TINY * w[1][e].abs().sum(1)
+                tol = 1.1 * da * (b.abs() + db) + sl.abs() * db \
                     + 2.0 ** -21 * (4 + a.abs()) * ref.abs() + 1e-30
-            tol = tol + 2.0 ** -8 * (ref.abs() + tol)
+            tol = tol + 2.0 ** -8 * (ref.abs() + tol) + 2.0 ** -134
             bad = ((out[r].double() - ref).abs() > tol)
             assert not bool(bad.any()), (e, int(bad.sum()), bad.nonzero()[0].tolist())
         outside = torch.ones(self.R, dtype=torch.bool)
@@ -186,6 +194,66 @@ def test_bad_tokens_and_offsets(mats):
     p.run()
     assert M.moe_check_error(p.ws) == M.MOE_ERR_DEVICE_CHECK
     assert torch.equal(p.out[:9], good[:9]) and bool((p.out[9:] == 7.0).all())
+
+
+@pytest.mark.parametrize("mats", [1, 2])
+@pytest.mark.parametrize("group", [64, 128])
+def test_few_rows_of_any_magnitude(group, mats):
+    # rows of a few tokens (the digits form): magnitudes from 2^-100 to 2^60
+    # within a row, rows of one size, of zeros, of a bf16's smallest and largest.
+    # An input below 2^-22 of the largest of its 128 is off by 2^-31 of it at
+    # most: 2^-31 sum |w| max |x| more, which 2^-23 S covers 256 times over
+    # wherever the largest input's weight is not 0
+    p = Problem([1, 2, 3, 4, 5, 8], 72, 640, group, False, mats, seed=30)
+    g = torch.Generator(device="cuda").manual_seed(31)
+    e = torch.randint(-100, 60, (p.R, p.k), generator=g, device="cuda").double()
+    x = p.x.double()
+    x[0] *= 2.0 ** e[0]
+    x[1] = 0
+    x[2] *= 2.0 ** -100
+    x[3] *= 1e-38 / 8
+    x[4] *= 2.0 ** (e[4] / 16)
+    x[5, :128] = 0
+    x[6] = 1.0
+    x[7] *= 2.0 ** 60
+    p.x.copy_(x.to(BF))
+    for q, s in p.m:                                  # the largest input of every 128 has a weight
+        big = p.x.abs().reshape(p.R, -1, 128).argmax(-1) + torch.arange(p.k // 128, device="cuda") * 128
+        c = torch.stack((q & 15, q >> 4), -1).reshape(q.shape[0], q.shape[1], -1)
+        c[:, :, big.reshape(-1)] = 15
+        q.copy_(c[..., 0::2] | (c[..., 1::2] << 4))
+    p.run()
+    w = [dequantize(*m, group) for m in p.m]
+    if mats == 1:
+        p.check()
+        return
+    p.x[0], p.x[7] = p.x[6], p.x[6]                   # (silu's product of such magnitudes overflows)
+    p.run()
+    p.check()
+
+
+@pytest.mark.parametrize("mats", [1, 2])
+def test_few_rows_with_non_finite_inputs(mats):
+    p = Problem([3, 4, 1, 2], 72, 256, 64, False, mats, seed=32)
+    good = p.run().clone()
+    p.x[1, 5] = float("inf")
+    p.x[4, 9] = float("nan")
+    p.x[5, 200] = float("-inf")
+    out = p.run()
+    hit = torch.zeros(10, dtype=torch.bool)
+    hit[[1, 4, 5]] = True
+    # (a warp that meets a NaN computes its tile one by one: other rows of the
+    # expert agree to the tolerance, other experts' bit for bit)
+    other = torch.tensor([7, 8, 9])
+    assert torch.equal(out[other], good[other])
+    fine = (~hit).nonzero().flatten()
+    assert bool(((out[fine].double() - good[fine].double()).abs() <= 2.0 ** -7 * good[fine].double().abs() + 1e-3).all())
+    assert bool(out[4].isnan().all())
+    if mats == 1:
+        for r, e in ((1, 0), (5, 1)):
+            want = (p.x[r].double()[None, :] * dequantize(*p.m[0], 64)[e]).sum(1)
+            nan = want.isnan()
+            assert torch.equal(out[r].isnan(), nan) and torch.equal(out[r][~nan].double(), want[~nan])
 
 
 def test_no_rows():
