@@ -219,6 +219,10 @@ __device__ __forceinline__ void stage_mma(float (&acc)[2][TOK / 8][4], uint32_t 
   }
 }
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
+}
+
 template <bool SWIGLU, int NT, int GPC, bool DEEP>
 __global__ void __launch_bounds__(NUM_THREADS, W4Cfg<NT, GPC == 1, DEEP>::CTAS)
     w4_kernel(const __grid_constant__ W4Args g, const __grid_constant__ W4Tma m) {
@@ -236,6 +240,15 @@ __global__ void __launch_bounds__(NUM_THREADS, W4Cfg<NT, GPC == 1, DEEP>::CTAS)
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int E = g.E;
 
+  if (warp == 1 && lane < (g.t_shared > 0 ? 2 : 1)) {
+    prefetch_map(&m.q1[lane]);
+    prefetch_map(&m.s1[lane]);
+    prefetch_map(&m.x[lane]);
+    if (SWIGLU) {
+      prefetch_map(&m.q3[lane]);
+      prefetch_map(&m.s3[lane]);
+    }
+  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 4); }
     *abort_flag = 0;
@@ -339,9 +352,7 @@ __global__ void __launch_bounds__(NUM_THREADS, W4Cfg<NT, GPC == 1, DEEP>::CTAS)
       }
       const uint32_t tx = W_BYTES + (uint32_t)(WR * NG * 2) + (uint32_t)(nx * 4 * KS * 2);
       for (int kb = 0; kb < ks; ++kb) {
-        int w = 1;
-        if (lane == 0) w = mbar_wait(&empty[s], ph ^ 1, abort_flag, g.err) ? 1 : 0;
-        if (!__shfl_sync(0xffffffffu, w, 0)) { ok = false; break; }
+        if (!__all_sync(0xffffffffu, mbar_wait(&empty[s], ph ^ 1, abort_flag, g.err))) { ok = false; break; }
         uint8_t* sw = tiles + s * C::STAGE_BYTES;
         uint8_t* sx = sw + W_BYTES;
         uint8_t* ss = sx + C::X_BYTES;
@@ -394,9 +405,8 @@ __global__ void __launch_bounds__(NUM_THREADS, W4Cfg<NT, GPC == 1, DEEP>::CTAS)
   int s = 0;
   uint32_t ph = 0;
   for (;;) {
-    int ok = 1;
-    if (lane == 0) ok = mbar_wait(&full[s], ph, abort_flag, g.err) ? 1 : 0;
-    if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+    bool ok = __all_sync(0xffffffffu, mbar_wait(&full[s], ph, abort_flag, g.err));
+    if (!ok) break;
     const W4Tile t = info[s];
     if (t.rows < 0) break;
     const int ks = (g.k[t.kind] + KS - 1) / KS;
@@ -409,8 +419,7 @@ __global__ void __launch_bounds__(NUM_THREADS, W4Cfg<NT, GPC == 1, DEEP>::CTAS)
         for (int q = 0; q < 4; ++q) acc[a][n][q] = 0.f;
     for (int kb = 0; kb < ks; ++kb) {
       if (kb > 0) {
-        if (lane == 0) ok = mbar_wait(&full[s], ph, abort_flag, g.err) ? 1 : 0;
-        ok = __shfl_sync(0xffffffffu, ok, 0);
+        ok = __all_sync(0xffffffffu, mbar_wait(&full[s], ph, abort_flag, g.err));
         if (!ok) break;
       }
       const uint32_t st = base + s * C::STAGE_BYTES;
