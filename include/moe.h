@@ -302,14 +302,22 @@ MOE_API moe_status moe_forward_fp8(const moe_config* cfg, int64_t T, const void*
  * rounded to the output's type once. offsets is read on the device: an expert
  * whose pair of offsets is not 0 <= offsets[e] <= offsets[e+1] <= R sets
  * MOE_ERR_DEVICE_CHECK in the workspace's error word and counts as one
- * without rows (a row that two experts' ranges then share takes either's
- * result). Experts may have no rows; rows of y and dx outside every expert's
- * range are not written. */
+ * without rows. (The ranges left may then overlap: a row that two share takes
+ * either's result, and when they hold more than R rows together any row of y
+ * or dx may be left as it was.) Experts may have no rows; rows of y and dx
+ * outside every expert's range are not written. An output must not overlap an
+ * input. bf16 calls run on the CUDA cores under MOE_EXPERT_KERNEL_SIMT.
+ *
+ * The kernels of this section and of the 4-bit one are launched as
+ * programmatic dependents of what is before them in the stream: their set-up
+ * overlaps that kernel's end, and they read and write tensors only after it is
+ * complete. The calls can be captured into a CUDA graph and replayed with
+ * other offsets, src and data in the same buffers. */
 typedef struct {
-  int64_t rows;       /* R: 0 <= R < 2^31. With R == 0 the row matrices may be NULL */
+  int64_t rows;       /* R: 0 <= R <= 2^30. With R == 0 the row matrices may be NULL */
   int32_t n_experts;  /* E: 1 <= E <= 1024 */
   int32_t n;          /* N: outputs of an expert's matrix, a multiple of 8 (bf16) / 4 (fp32) */
-  int32_t k;          /* K: its inputs, likewise; N, K <= 2^20 and N, E * K < 2^31 */
+  int32_t k;          /* K: its inputs, likewise; N, K <= 2^20 and E * N * K <= 2^39 */
   int32_t dtype;      /* moe_dtype */
 } moe_grouped_shape;
 
@@ -353,13 +361,15 @@ typedef struct {
  * each group's scale is its largest magnitude / 7 rounded to bf16 (1 for a
  * group of zeros or one whose quotient rounds to 0), each code the nearest
  * integer (ties to even) to w / scale, plus 8, clamped to 0..15. A group that
- * holds a NaN or an infinity stands for NaNs. K must be a multiple of group, N of 8. */
+ * holds a NaN or an infinity stands for NaNs. K must be a multiple of group,
+ * N of 8. */
 MOE_API moe_status moe_quantize_w4(const moe_grouped_shape* g, int32_t group, const void* w,
                                    void* q, void* scales, void* stream);
 
 /* Products with 4-bit matrices, bf16 activations: expert e's row r reads
  * token src[r] of x [x_rows, K] (x_rows >= 1 unless R == 0), or row r itself
- * when src is NULL (then x_rows must be R). Sums in fp32, scales applied in fp32, one rounding:
+ * when src is NULL (then x_rows must be R). Sums in fp32, scales applied in
+ * fp32, one rounding:
  *
  *   moe_grouped_matvec_w4   y[r] = W_e x[src[r]]
  *   moe_grouped_swiglu_w4   h[r] = silu(W1_e x[src[r]]) * (W3_e x[src[r]])
@@ -481,8 +491,9 @@ MOE_API moe_status moe_stage_timing_begin_every(int32_t max_calls, int32_t every
  *   TCGEN05         tensor cores, expert GEMM always with one CTA per tile;
  *   TCGEN05_PAIR    tensor cores, expert GEMM always on CTA pairs;
  *   SIMT            the CUDA-core kernels that fp32 layers always use, for
- *                   both the router logits and the expert GEMMs: a slow,
- *                   independent cross-check of the tensor-core kernels.
+ *                   the router logits, the expert GEMMs and the grouped
+ *                   products: a slow, independent cross-check of the
+ *                   tensor-core kernels.
  * Returns MOE_ERR_INVALID_ARG for other values. */
 enum {
   MOE_EXPERT_KERNEL_AUTO = 0,
@@ -518,7 +529,9 @@ MOE_API int32_t moe_fp8_kernel_for(const moe_config* cfg, int64_t T);
  * nothing completes:
  *   1  the up-projection of every bf16 layer on the one-CTA tensor-core
  *      kernel, and of every FP8 layer in either form (the rows of that
- *      CTA's tiles are not written);
+ *      CTA's tiles are not written); the bf16 grouped products on the tensor
+ *      cores, the products with 4-bit weights, and moe_forward_w4's
+ *      up-projection (likewise, or those elements of dw);
  *   2  the tensor-core router logits of every bf16 layer (that CTA's partial
  *      sums are not written).
  * The wait runs out after its 1 s limit; the launch then takes the abort

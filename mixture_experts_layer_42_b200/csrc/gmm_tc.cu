@@ -26,10 +26,10 @@
 // the MMA issuer, warps 2-9 the epilogue (two warps on each 32 TMEM lanes, in
 // turn over the columns), warp 10 the scheduler, which works the tiles out
 // ahead of the others. Rows leave through a warp's own shared memory (the
-// accumulator holds features by rows), dw straight from registers. Rows of a tile past its expert's
-// end are other rows of the matrix (their columns are not stored); only DW,
-// which sums over rows, reads through per-expert maps that end at the
-// expert's last row. Every wait is bounded (1 s); on expiry the kernel raises
+// accumulator holds features by rows), dw straight from registers. Rows of a
+// tile past its expert's end are other rows of the matrix (their columns are
+// not stored); only DW, which sums over rows, reads through per-expert maps
+// that end at the expert's last row. Every wait is bounded (1 s); on expiry the kernel raises
 // the error word's timeout bit, drains its copies and returns.
 #include "api_common.cuh"
 #include "gmm.cuh"
@@ -53,16 +53,14 @@ constexpr int MAX_E = 1024;
 constexpr int NBOX = 9;                   // row boxes of 8, 16, 32, 48, ... 128 rows
 constexpr int SLOTS = 12;                 // stages in flight, at most
 constexpr int TQ = 4;                     // tiles the scheduler works out ahead
-constexpr int HEAVY = 256;                // rows above which an expert's tiles count as heavy
 
 template <int MODE> struct Cfg {
   static constexpr int HALVES = MODE == GMM_DW ? 1 : 2;
   static constexpr int RING = MODE == GMM_DW ? 6 * 2 * TILE : 192 * 1024;
   // staging of an epilogue warp: 32 rows x 32 features in bf16
   static constexpr int STG = MODE == GMM_DW ? 0 : 2048;
-  // experts' first rows and counts, and (FWD, DX) the tile prefixes of the
-  // heavy and of the light ones
-  static constexpr int TABLE = (MODE == GMM_DW ? 2 : 4) * (MAX_E + 1) * 4;
+  // experts' first rows and counts, and (FWD, DX) the prefixes of their tiles
+  static constexpr int TABLE = (MODE == GMM_DW ? 2 : 3) * (MAX_E + 1) * 4;
   static constexpr size_t SMEM = 1024 + RING + 8 * STG + 512 + TABLE;
 };
 
@@ -95,20 +93,19 @@ struct Tile {
 struct Sched {
   const int32_t* off;  // smem: first row and number of rows of each expert
   const int32_t* cnt;
-  const int32_t* PH;   // smem: token-tile prefixes over experts [E + 1], of the heavy ones
-  const int32_t* PL;   // and of the light ones (FWD, DX)
-  int E, nf, nc, heavy, total, n, k;
+  const int32_t* P;    // smem: token-tile prefixes over experts [E + 1] (FWD, DX)
+  int E, nf, nc, total, n, k;
 };
 
 __device__ __forceinline__ int round32(int v) { return (v + 31) & ~31; }
 __device__ __forceinline__ int tile_rows(int count, int mt) { return round32((count + mt - 1) / mt); }
 
-// Tile i of the launch. DW: expert by expert. FWD, DX: the tiles of the heavy
-// experts (many rows: bound by the MMAs) and of the light ones (few: bound by
-// their weights' bytes) in even turns, so that both run at any time and the
-// pairs' mixtures are alike; within each, expert by expert, its feature
-// blocks, and the row tiles that share them side by side (expert e's rows in
-// mt tiles of tile_rows each).
+// Tile i of the launch, expert by expert: its feature blocks, and the tiles
+// that share a block's weights (FWD, DX: expert e's rows in mt tiles of
+// tile_rows each) side by side. The experts' own order stands: the tiles of
+// experts with many rows and of those with few in even turns, so that the MMAs
+// of the one kind would run beside the other's bytes, took 1814 instead of
+// 1518 us of 32768 skewed rows (Zipf 1.2 over 256 experts of 2048 x 7168).
 template <int MODE>
 __device__ __forceinline__ Tile decode(const Sched& S, int i) {
   Tile t;
@@ -124,10 +121,7 @@ __device__ __forceinline__ Tile decode(const Sched& S, int i) {
     t.depth = S.cnt[t.e];
     t.r0 = S.off[t.e];
   } else {
-    const int h1 = (int)((int64_t)(i + 1) * S.heavy / S.total);  // heavy tiles up to and with i
-    const bool hv = h1 > (int)((int64_t)i * S.heavy / S.total);
-    const int32_t* P = hv ? S.PH : S.PL;
-    i = hv ? h1 - 1 : i - h1;
+    const int32_t* P = S.P;
     const int q = i / S.nf;
     int lo = 0, hi = S.E;  // the e with P[e] <= q < P[e + 1]
     while (hi - lo > 1) {
@@ -421,8 +415,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
   Tile* tq = reinterpret_cast<Tile*>(tmem_slot + 4);  // [TQ]
   int32_t* cnt = reinterpret_cast<int32_t*>(stage_out + 8 * C::STG + 512);
   int32_t* off = cnt + MAX_E + 1;
-  int32_t* PH = off + MAX_E + 1;
-  int32_t* PL = PH + MAX_E + 1;
+  int32_t* P = off + MAX_E + 1;
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t rank = cluster_rank();
@@ -613,10 +606,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     }
   } else if (warp == 10) {
     // ---------------------------------------------------------------- scheduler (both CTAs)
+    int64_t rows = 0;  // of all experts
     if (MODE != GMM_DW) {
       const int per = (E + 31) / 32;
       int maxc = 0;
-      int64_t rows = 0;
       int tl[5] = {0, 0, 0, 0, 0};  // tiles at a cap of 512, 256, 128, 64, 32 rows
       for (int u = 0; u < per; ++u) {
         const int e = lane * per + u;
@@ -629,7 +622,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       }
       // The rows a tile may hold. What bounds large calls is the traffic from
       // L2, 256 + rows per tile and 64 of the reduction, shared by the pairs;
-      // a small call also waits for its last tile, up to 256 + cap.
+      // a small call also waits for its last tile, up to 256 + cap (against
+      // 512 always: 8192 rows of 8 experts of 1024 x 2048 34 instead of 50 us,
+      // 300 rows of one 2048 x 2048 17 instead of 21; 15.4 instead of 14.9 for
+      // 2048 rows of 16 of 1024 x 1024).
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) {
         maxc = max(maxc, __shfl_xor_sync(0xffffffffu, maxc, o));
@@ -646,30 +642,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         const int64_t cost = tl[c] * (int64_t)nf <= npairs ? most : all + most;
         if (cost < best) { best = cost; cap = 512 >> c; }
       }
-      int sum[2] = {0, 0};  // token tiles of this lane's light and heavy experts
+      int sum = 0;  // token tiles of this lane's experts
       for (int u = 0; u < per; ++u) {
         const int e = lane * per + u;
-        if (e < E) sum[cnt[e] > HEAVY] += (int)(((int64_t)cnt[e] + cap - 1) / cap);
+        if (e < E) sum += (int)(((int64_t)cnt[e] + cap - 1) / cap);
       }
-      int run[2];
+      int incl = sum;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        int incl = sum[h];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int p = __shfl_up_sync(0xffffffffu, incl, o);
-          if (lane >= o) incl += p;
-        }
-        run[h] = incl - sum[h];
-        if (lane == 31) (h ? PH : PL)[E] = incl;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int p = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += p;
       }
+      if (lane == 31) P[E] = incl;
+      int run = incl - sum;
       for (int u = 0; u < per; ++u) {
         const int e = lane * per + u;
         if (e < E) {
-          PL[e] = run[0];
-          PH[e] = run[1];
-          const int mt = (int)(((int64_t)cnt[e] + cap - 1) / cap);
-          if (cnt[e] > HEAVY) run[1] += mt; else run[0] += mt;
+          P[e] = run;
+          run += (int)(((int64_t)cnt[e] + cap - 1) / cap);
         }
       }
     }
@@ -677,15 +667,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     Sched S;
     S.off = off;
     S.cnt = cnt;
-    S.PH = PH;
-    S.PL = PL;
+    S.P = P;
     S.E = E;
     S.nf = nf;
     S.nc = (g.k + MAXN - 1) / MAXN;
     S.n = g.n;
     S.k = g.k;
-    S.heavy = MODE == GMM_DW ? 0 : nf * PH[E];
-    S.total = MODE == GMM_DW ? E * nf * S.nc : S.heavy + nf * PL[E];
+    // more rows than there are: bad offsets whose ranges overlap (reported
+    // above), and a sum of tiles that may pass an int: none then
+    S.total = MODE == GMM_DW ? E * nf * S.nc : rows > g.rows ? 0 : nf * P[E];
     uint32_t q = 0, ph = 0;
     for (int i = pair;; i += npairs) {
       Tile t;

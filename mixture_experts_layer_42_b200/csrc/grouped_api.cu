@@ -31,10 +31,10 @@ moe_status check_shape(const moe_grouped_shape* g) {
   const int q = g->dtype == MOE_DT_BF16 ? 8 : 4;  // 16-byte rows
   if (g->rows < 0 || g->n_experts < 1 || g->n < 1 || g->k < 1) return MOE_ERR_INVALID_ARG;
   if (g->n % q || g->k % q) return MOE_ERR_INVALID_ARG;
+  // tile counts, rows and the weights' strides in the kernels' and the maps' types
   if (g->n_experts > 1024 || g->n > (1 << 20) || g->k > (1 << 20)) return MOE_ERR_UNSUPPORTED;
-  if ((int64_t)g->n_experts * (g->n > g->k ? g->n : g->k) > (int64_t)INT32_MAX)
-    return MOE_ERR_UNSUPPORTED;
-  if (g->rows > (int64_t)INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  if ((int64_t)g->n_experts * g->n > ((int64_t)1 << 39) / g->k) return MOE_ERR_UNSUPPORTED;
+  if (g->rows > (int64_t)1 << 30) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
@@ -122,6 +122,7 @@ moe_status run_w4(const moe_grouped_shape* g, int group, int64_t x_rows, const v
   p.rows = g->rows;
   p.E = g->n_experts;
   p.group = group;
+  p.stall = pipeline_stall() == STALL_EXPERTS_UP;
   p.err = at<uint32_t>(ws, 0);
   return cuda_status(launch_w4(swiglu, p, num_sms_current(), s));
 }
@@ -274,9 +275,11 @@ moe_status moe_forward_w4(const moe_config* cfg, int64_t T, const void* x, const
   p.E = c.n_routed;
   p.group = w->group;
   p.t_shared = sh ? T : 0;
+  p.stall = pipeline_stall() == STALL_EXPERTS_UP;
   p.err = err;
   if (launch_w4(true, p, num_sms_current(), s) != cudaSuccess) return MOE_ERR_CUDA;
   // down: from h in the expert order into y_perm, from the shared h into s
+  p.stall = 0;
   void* sbuf = sh ? at<void>(ws, L.s) : nullptr;
   p.x[0] = at<__nv_bfloat16>(ws, L.h);
   p.x[1] = at<__nv_bfloat16>(ws, L.hs);

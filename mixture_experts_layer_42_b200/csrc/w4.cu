@@ -5,6 +5,7 @@
 
 #include "api_common.cuh"
 
+#include <cfloat>
 #include <cstring>
 
 #include "tc_common.cuh"
@@ -37,7 +38,7 @@ __global__ void __launch_bounds__(256) quantize_w4_kernel(const T* w, int64_t ro
   for (int u = 0; u < 8; ++u) {
     v[u] = j < k ? to_f32(w[row * k + j + u]) : 0.f;
     m = fmaxf(m, fabsf(v[u]));
-    bad |= !(fabsf(v[u]) <= 3.4e38f);
+    bad |= !(fabsf(v[u]) <= FLT_MAX);
   }
   uint32_t badm = bad;
   for (int o = 1; o < group / 8; o <<= 1) {
@@ -237,6 +238,7 @@ __global__ void __launch_bounds__(NUM_THREADS, W4Cfg<NT, GPC == 1, DEEP>::CTAS)
   W4Tile* info = reinterpret_cast<W4Tile*>(empty + STAGES);  // [STAGES]: the tile a stage begins
   volatile int* abort_flag = reinterpret_cast<volatile int*>(info + STAGES);
   int32_t* P = reinterpret_cast<int32_t*>(tiles + STAGES * C::STAGE_BYTES + 256);
+  uint64_t* hang = reinterpret_cast<uint64_t*>(tiles + STAGES * C::STAGE_BYTES + 248);  // (see W4Args::stall)
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int E = g.E;
 
@@ -251,6 +253,7 @@ __global__ void __launch_bounds__(NUM_THREADS, W4Cfg<NT, GPC == 1, DEEP>::CTAS)
   }
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 4); }
+    mbar_init(hang, 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -272,18 +275,21 @@ __global__ void __launch_bounds__(NUM_THREADS, W4Cfg<NT, GPC == 1, DEEP>::CTAS)
     // ---------------------------------------------------------------- TMA producer
     // the tiles' exclusive prefix over the experts
     const int per = (E + 31) / 32;
-    int lsum = 0;
+    int64_t lsum = 0;
     for (int u = 0; u < per; ++u) {
       const int e = lane * per + u;
       if (e < E) lsum += P[e];
     }
-    int incl = lsum;
+    int64_t incl = lsum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int p = __shfl_up_sync(0xffffffffu, incl, o);
+      const int64_t p = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += p;
     }
-    int run = incl - lsum;
+    // more tiles than the rows can fill: bad offsets whose ranges overlap
+    // (reported above), and a sum that may pass an int: none then
+    const bool over = __shfl_sync(0xffffffffu, incl, 31) > g.rows / TOK + E;
+    int run = (int)(incl - lsum);
     for (int u = 0; u < per; ++u) {
       const int e = lane * per + u;
       if (e < E) {
@@ -292,7 +298,7 @@ __global__ void __launch_bounds__(NUM_THREADS, W4Cfg<NT, GPC == 1, DEEP>::CTAS)
         run += c;
       }
     }
-    if (lane == 31) P[E] = incl;
+    if (lane == 31) P[E] = over ? 0 : (int)incl;
     __syncwarp();
     const int nt0 = (g.n[0] + FW - 1) / FW, nt1 = (g.n[1] + FW - 1) / FW;
     const int mt_sh = (int)((g.t_shared + TOK - 1) / TOK);
@@ -384,7 +390,9 @@ __global__ void __launch_bounds__(NUM_THREADS, W4Cfg<NT, GPC == 1, DEEP>::CTAS)
     // unevenly while this one's still run (one token's up-projection: 50
     // instead of 39 us a call).
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (!ok && lane == 0)
+    // after a wait that ran out, in any warp: no copy may still be under way
+    __syncthreads();
+    if (*abort_flag && lane == 0)
       for (int j = 0; j < STAGES; ++j) {
         const int n = issued / STAGES + (j < issued % STAGES ? 1 : 0);
         if (n > 0) mbar_drain(&full[j], (uint32_t)((n - 1) & 1));
@@ -404,8 +412,10 @@ __global__ void __launch_bounds__(NUM_THREADS, W4Cfg<NT, GPC == 1, DEEP>::CTAS)
   const uint32_t o_s = (uint32_t)(W_BYTES + C::X_BYTES + row * 2);
   int s = 0;
   uint32_t ph = 0;
-  for (;;) {
-    bool ok = __all_sync(0xffffffffu, mbar_wait(&full[s], ph, abort_flag, g.err));
+  bool ok = true;
+  if (g.stall && blockIdx.x == 0 && w == 0) ok = __all_sync(0xffffffffu, mbar_wait(hang, 0, abort_flag, g.err));
+  while (ok) {
+    ok = __all_sync(0xffffffffu, mbar_wait(&full[s], ph, abort_flag, g.err));
     if (!ok) break;
     const W4Tile t = info[s];
     if (t.rows < 0) break;
@@ -457,6 +467,7 @@ __global__ void __launch_bounds__(NUM_THREADS, W4Cfg<NT, GPC == 1, DEEP>::CTAS)
         }
     }
   }
+  __syncthreads();  // (the producer's)
 }
 
 }  // namespace
@@ -521,9 +532,13 @@ cudaError_t launch_w4_group(const W4Args& g, const W4Tma& m, int64_t bound, int 
 
 template <bool SWIGLU>
 cudaError_t launch_w4_tokens(const W4Args& g, const W4Tma& m, int64_t bound, int num_sms, cudaStream_t st) {
-  // token rows per tile, by the rows an expert has on average
+  // Token rows per tile, by the rows an expert has on average: more rows share
+  // their weights' way to operands, fewer leave less padding and more stages.
+  // Down-projection of 256 experts of 7168 x 2048 with 8 / 16 / 32: 417 / 440 /
+  // 451 us at 4 rows, 450 / 464 / 477 at 5, 493 / 485 / 496 at 6, 700 / 573 /
+  // 577 at 10, 811 / 659 / 620 at 12.
   const int64_t avg = g.rows / g.E;
-  if (avg > 12) return launch_w4_group<SWIGLU, 4, false>(g, m, bound, num_sms, st);
+  if (avg > 10) return launch_w4_group<SWIGLU, 4, false>(g, m, bound, num_sms, st);
   if (avg > 5) return launch_w4_group<SWIGLU, 2, false>(g, m, bound, num_sms, st);
   if (bound <= 2 * (int64_t)num_sms) return launch_w4_group<SWIGLU, 1, true>(g, m, bound, num_sms, st);
   return launch_w4_group<SWIGLU, 1, false>(g, m, bound, num_sms, st);
@@ -547,7 +562,7 @@ cudaError_t launch_w4(bool swiglu, const W4Args& g, int num_sms, cudaStream_t st
     if (swiglu && (!map_u8_3d(&m.q3[kind], g.q3[kind], E, n, k / 2, fw) ||
                    !map_scales(&m.s3[kind], g.s3[kind], E, k / g.group, n, fw, KS / g.group)))
       return cudaErrorInvalidValue;
-    bound += (int64_t)ceil_div(n, (int)fw) * (rows / 8 + (kind == 0 && rows > E ? E : rows));
+    bound += (int64_t)ceil_div(n, (int)fw) * (rows / 8 + (rows > E ? E : rows));
   }
   if (bound == 0) return cudaSuccess;
   return swiglu ? launch_w4_tokens<true>(g, m, bound, num_sms, st)

@@ -22,6 +22,7 @@ struct W4Args {
   int64_t rows;
   int E, group;
   int64_t t_shared;
+  int stall;                  // test hook: CTA 0's first multiplying warp lets a wait run out
   uint32_t* err;
 };
 

@@ -9,6 +9,8 @@ core may truncate), so (d + 2) 2^-23 S in all; the rounding of the result to
 its type adds eps / 2 of it (2^-8 of a bf16 result), and an accumulated call
 one more fp32 addition."""
 
+import time
+
 import pytest
 import torch
 
@@ -240,6 +242,37 @@ def test_bad_offsets_are_reported_and_skipped(dtype, op):
         ref, S = rows @ w, rows.abs() @ w.abs()
         eps = torch.finfo(dtype).eps / 2
         assert bool(((out[20:60].double() - ref).abs() <= eps * ref.abs() * 1.01 + 74 * 2.0 ** -23 * S).all())
+
+
+@pytest.mark.parametrize("op", ["fwd", "dx"])
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_offsets_that_go_back_and_forth(dtype, op):
+    # each second pair is bad, the others all hold every row: more tiles than
+    # the launch has, and a sum past 2^31 rows
+    E, R = 1024, 1 << 22
+    p = Problem([0] * E, 8, 8, dtype, tail=R, seed=12)
+    p.offsets.copy_(torch.tensor([0, R] * (E // 2) + [0], dtype=torch.int32))
+    p.run(op)
+    assert M.moe_check_error(p.ws) == M.MOE_ERR_DEVICE_CHECK
+    assert M.moe_check_error(p.ws) == M.MOE_OK
+
+
+@pytest.mark.parametrize("op", ["fwd", "dx", "dw"])
+def test_a_wait_that_runs_out_is_reported(op):
+    # the first pair's MMA warp waits on a barrier that nothing completes: the
+    # call ends after the limit, and the next one is right
+    p = Problem([300, 0, 200], 328, 456, BF, seed=13)
+    M.moe_debug_stall_pipeline(1)
+    try:
+        t0 = time.time()
+        p.run(op)
+        status = M.moe_check_error(p.ws)
+        elapsed = time.time() - t0
+    finally:
+        M.moe_debug_stall_pipeline(0)
+    assert status == M.MOE_ERR_TIMEOUT
+    assert 0.9 < elapsed < 30
+    p.check(op, p.run(op))
 
 
 @pytest.mark.parametrize("op", ["fwd", "dx", "dw"])

@@ -33,12 +33,13 @@ def size(M, **kw):
 
 
 @pytest.mark.parametrize("kw,status", [
-    ({}, 0), (dict(rows=0), 0), (dict(rows=(1 << 31) - 1), 0),
+    ({}, 0), (dict(rows=0), 0), (dict(rows=1 << 30), 0),
     (dict(rows=-1), -1), (dict(n_experts=0), -1), (dict(n=0), -1), (dict(k=0), -1),
     (dict(n=12), -1), (dict(k=4), -1), (dict(dtype=2), -1),
     (dict(dtype=0, n=12, k=4), 0), (dict(dtype=0, n=6), -1),
-    (dict(rows=1 << 31), -2), (dict(n_experts=1025), -2), (dict(n=(1 << 20) + 8), -2),
-    (dict(n_experts=1024, n=1 << 20, k=1 << 20), 0), (dict(n_experts=1024), 0),
+    (dict(rows=(1 << 30) + 1), -2), (dict(rows=1 << 31), -2), (dict(n_experts=1025), -2), (dict(n=(1 << 20) + 8), -2),
+    (dict(n_experts=1024, n=1 << 20, k=1 << 9), 0), (dict(n_experts=1024), 0),
+    (dict(n_experts=1024, n=1 << 20, k=1 << 10), -2), (dict(n_experts=1, n=1 << 20, k=1 << 20), -2),
 ])
 def test_shapes(M, kw, status):
     st, n = size(M, **kw)
