@@ -25,64 +25,75 @@ template <> __device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bf
 
 constexpr int GTHREADS = 64;
 
-// A tile of M x N by 64 threads, each 4 RM rows x 4 CN columns, in slices of
-// K of the reduction. What bounds large calls is the fma pipe, and next to it
-// shared memory's reads: 16 x 8 a thread needs 6 reads of 16 bytes for 64
-// packed fmas (8 x 8 needs 4 for 32, and shared memory bounds it: 590 us of
-// the odd fp32 input gradient's sizes against 540). Calls whose large tiles
-// would not fill the GPU take small ones, whose K is deep because latency
-// counts (19 -> 6 us for the tiny layer's up-projection).
-struct Large { static constexpr int M = 64, N = 128, K = 8, RM = 4, CN = 2, CTAS = 4; };
-struct Small { static constexpr int M = 16, N = 64, K = 32, RM = 1, CN = 1, CTAS = 4; };
+// A tile of M x N by 64 threads, each R rows x Q columns, in slices of K of the
+// reduction, CTAS blocks per SM. What bounds large calls is the fma pipe, with
+// few warps to hide its latency, and the last wave of tiles. 4084 skewed rows
+// of 16 experts of 1032 x 2052: dx 415 us, dw 377 us (46 of the pipe's 74 TF),
+// the product 556 us; tiles of 64 x 128 with 16 x 8 a thread (two warps a
+// scheduler) and transposed slices took 442, 398 and 760 us. More blocks an SM
+// spill (the product with 5: 997 us). Calls of few such tiles take small ones,
+// whose K is deep because latency counts (19 -> 5 us for the tiny layer's
+// up-projection).
+struct Large { static constexpr int M = 64, N = 64, K = 16, R = 8, Q = 8, CTAS = 5, CTAS_FWD = 4; };
+struct Small { static constexpr int M = 16, N = 64, K = 32, R = 4, Q = 4, CTAS = 4, CTAS_FWD = 4; };
 
-// An operand slice of W x K in registers, then in shared memory by t: S[t][i].
-// ALONG_T: t is contiguous in memory (element (i, t) at p[i * ld + t]), else i
-// is (p[t * ld + i]). Out-of-range elements read as zeros.
+// An operand's slice of W x K in shared memory, as it lies in memory: ALONG_T
+// (t is contiguous, element (i, t) at p[i * ld + t]) by i, S[i][t], else (p[t *
+// ld + i]) by t, S[t][i]. Out-of-range elements read as zeros. fp32 is copied
+// asynchronously, bf16 widened through registers.
 template <typename T, bool ALONG_T, int W, int K>
 struct Slice {
-  static constexpr int LD = W + 4;
-  static constexpr int NV = W * K / 4 / GTHREADS;  // float4s a thread carries
-  float4 v[NV];
-  static constexpr int TPT = GTHREADS / K;         // threads per t (not ALONG_T)
-  __device__ __forceinline__ static int at_i(int u) {
-    return ALONG_T ? (threadIdx.x + GTHREADS * u) % W : (threadIdx.x % TPT + TPT * u) * 4;
-  }
-  __device__ __forceinline__ static int at_t(int u) {
-    return ALONG_T ? (threadIdx.x + GTHREADS * u) / W * 4 : threadIdx.x / TPT;
+  static constexpr bool ASYNC = sizeof(T) == 4;
+  static constexpr int ROWS = ALONG_T ? W : K, LEN = ALONG_T ? K : W;
+  static constexpr int LD = LEN + 4;               // no bank twice among 8 rows
+  static constexpr int NV = W * K / 4 / GTHREADS;  // float4s of a thread
+  using Tile = float[ROWS][LD];
+  float4 v[ASYNC ? 1 : NV];
+  // float4 u of this thread: its row and column of the slice
+  __device__ __forceinline__ static int row(int u) { return (threadIdx.x + GTHREADS * u) / (LEN / 4); }
+  __device__ __forceinline__ static int col(int u) { return (threadIdx.x + GTHREADS * u) % (LEN / 4) * 4; }
+  // its address, or null out of range
+  __device__ __forceinline__ static const T* at(int u, const T* p, int64_t ld, int i0, int ni, int t0,
+                                                int64_t nt) {
+    const int i = i0 + (ALONG_T ? row(u) : col(u)), t = t0 + (ALONG_T ? col(u) : row(u));
+    return i < ni && t < nt ? p + (ALONG_T ? (int64_t)i * ld + t : (int64_t)t * ld + i) : nullptr;
   }
   __device__ __forceinline__ void load(const T* p, int64_t ld, int i0, int ni, int t0, int64_t nt) {
+    if (ASYNC) return;
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
-      const int i = i0 + at_i(u), t = t0 + at_t(u);
-      v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (i < ni && t < nt) v[u] = load4<T>(p + (ALONG_T ? (int64_t)i * ld + t : (int64_t)t * ld + i));
+      const T* q = at(u, p, ld, i0, ni, t0, nt);
+      v[u] = q ? load4<T>(q) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
   }
-  __device__ __forceinline__ void store(float (*S)[LD]) const {
+  __device__ __forceinline__ void store(Tile& S) const {
+    if (ASYNC) return;
+#pragma unroll
+    for (int u = 0; u < NV; ++u) *reinterpret_cast<float4*>(&S[row(u)][col(u)]) = v[u];
+  }
+  __device__ __forceinline__ static void copy(Tile& S, const T* p, int64_t ld, int i0, int ni, int t0, int64_t nt) {
+    if (!ASYNC) return;
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
-      const int i = at_i(u), t = at_t(u);
-      if (ALONG_T) {
-        S[t + 0][i] = v[u].x;
-        S[t + 1][i] = v[u].y;
-        S[t + 2][i] = v[u].z;
-        S[t + 3][i] = v[u].w;
-      } else {
-        *reinterpret_cast<float4*>(&S[t][i]) = v[u];
-      }
+      const T* q = at(u, p, ld, i0, ni, t0, nt);
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                       (uint32_t)__cvta_generic_to_shared(&S[row(u)][col(u)])),
+                   "l"(q ? q : p), "r"(q ? 16 : 0)
+                   : "memory");
     }
   }
 };
 
+// Which row (column) of the tile a thread's q-th is, of NT threads side by
+// side: of a slice by i every NT-th (8 threads' 16-byte reads then meet no bank
+// twice), of one by t four neighbours in one read.
+template <bool ALONG_T, int NT> __device__ __forceinline__ int owned(int q, int thread) {
+  return ALONG_T ? thread + NT * q : q / 4 * 4 * NT + thread * 4 + q % 4;
+}
+
 // (d0, d1) += (a0 b0, a1 b1): two fp32 fmas in one instruction.
 __device__ __forceinline__ void fma2(uint64_t& d, uint64_t a, uint64_t b) {
   asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
-}
-
-__device__ __forceinline__ uint64_t twice(float a) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(a));
-  return r;
 }
 
 // This CTA's expert and, for FWD and DX, its tile among the expert's rows:
@@ -131,42 +142,75 @@ __device__ __forceinline__ bool find_tile(const GmmArgs& g, int mi, int* e_out, 
   return s_e >= 0;
 }
 
-// A slice's products: a thread's 4 RMV rows by 4 CN columns.
-template <typename C, int RMV, int LDA, int LDB>
-__device__ __forceinline__ void multiply(uint64_t (&acc)[4 * C::RM][2 * C::CN], const float (*As)[LDA],
-                                         const float (*Bs)[LDB], int tm, int tn) {
-  constexpr int NTN = C::N / (4 * C::CN), NTM = GTHREADS / NTN;
-#pragma unroll 8
-  for (int t = 0; t < C::K; ++t) {
-    float a[4 * C::RM];
-    ulonglong2 b[C::CN];  // pairs of columns
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// A slice's products: RV of a thread's R rows by its Q columns. Two fmas an
+// instruction: where both operands lie by i, those of two t (a sum of the even
+// t and one of the odd; no operand moves), else those of two columns.
+template <int MODE, typename C, int RV, typename SA, typename SB, int NACC>
+__device__ __forceinline__ void multiply(uint64_t (&acc)[C::R][NACC], const typename SA::Tile& As,
+                                         const typename SB::Tile& Bs, int tm, int tn) {
+  constexpr int NTN = C::N / C::Q, NTM = GTHREADS / NTN;
 #pragma unroll
-    for (int h = 0; h < RMV; ++h)
-      *reinterpret_cast<float4*>(a + 4 * h) = *reinterpret_cast<const float4*>(&As[t][4 * NTM * h + 4 * tm]);
+  for (int t = 0; t < C::K; t += 4) {
+    float4 a[RV];  // MODE != DW: rows, four t
+    if (MODE != GMM_DW)
 #pragma unroll
-    for (int h = 0; h < C::CN; ++h)
-      b[h] = *reinterpret_cast<const ulonglong2*>(&Bs[t][4 * NTN * h + 4 * tn]);
+      for (int q = 0; q < RV; ++q)
+        a[q] = *reinterpret_cast<const float4*>(&As[owned<true, NTM>(q, tm)][t]);
+    if (MODE == GMM_FWD) {
 #pragma unroll
-    for (int i = 0; i < 4 * RMV; ++i) {
-      const uint64_t ai = twice(a[i]);
+      for (int j = 0; j < C::Q; ++j) {
+        const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(&Bs[owned<true, NTN>(j, tn)][t]);
 #pragma unroll
-      for (int h = 0; h < C::CN; ++h) {
-        fma2(acc[i][2 * h], ai, b[h].x);
-        fma2(acc[i][2 * h + 1], ai, b[h].y);
+        for (int q = 0; q < RV; ++q) {
+          fma2(acc[q][j], pair(a[q].x, a[q].y), b.x);
+          fma2(acc[q][j], pair(a[q].z, a[q].w), b.y);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        ulonglong2 b[C::Q / 4];
+#pragma unroll
+        for (int h = 0; h < C::Q / 4; ++h)
+          b[h] = *reinterpret_cast<const ulonglong2*>(&Bs[t + v][owned<false, NTN>(4 * h, tn)]);
+        float4 d[RV / 4];  // DW: rows of this t
+        if (MODE == GMM_DW)
+#pragma unroll
+          for (int h = 0; h < RV / 4; ++h)
+            d[h] = *reinterpret_cast<const float4*>(&As[t + v][owned<false, NTM>(4 * h, tm)]);
+#pragma unroll
+        for (int q = 0; q < RV; ++q) {
+          const float x = MODE == GMM_DW ? reinterpret_cast<const float*>(&d[q / 4])[q % 4]
+                                         : reinterpret_cast<const float*>(&a[q])[v];
+          const uint64_t xx = pair(x, x);
+#pragma unroll
+          for (int h = 0; h < C::Q / 4; ++h) {
+            fma2(acc[q][2 * h], xx, b[h].x);
+            fma2(acc[q][2 * h + 1], xx, b[h].y);
+          }
+        }
       }
     }
   }
 }
 
 template <typename T, typename TO, int MODE, typename C>
-__global__ void __launch_bounds__(GTHREADS, C::CTAS) gmm_simt_kernel(const GmmArgs g) {
+__global__ void __launch_bounds__(GTHREADS, MODE == GMM_FWD ? C::CTAS_FWD : C::CTAS)
+    gmm_simt_kernel(const GmmArgs g) {
   constexpr int GM = C::M, GN = C::N, GK = C::K;
-  constexpr int NTN = GN / (4 * C::CN), NTM = GTHREADS / NTN;  // threads over columns, rows
-  static_assert(NTM * 4 * C::RM == GM, "threads cover the tile");
+  constexpr int NTN = GN / C::Q, NTM = GTHREADS / NTN;  // threads over columns, rows
+  static_assert(NTM * C::R == GM, "threads cover the tile");
   using SA = Slice<T, MODE != GMM_DW, GM, GK>;
   using SB = Slice<T, MODE == GMM_FWD, GN, GK>;
-  __shared__ __align__(16) float As[2][GK][SA::LD];
-  __shared__ __align__(16) float Bs[2][GK][SB::LD];
+  constexpr int NS = 3;  // slices in shared memory
+  __shared__ __align__(16) typename SA::Tile As[NS];
+  __shared__ __align__(16) typename SB::Tile Bs[NS];
   grid_dependency();
   const int tid = threadIdx.x;
   const int NJ = MODE == GMM_FWD ? g.n : g.k;
@@ -195,68 +239,85 @@ __global__ void __launch_bounds__(GTHREADS, C::CTAS) gmm_simt_kernel(const GmmAr
   const int64_t lda = MODE == GMM_FWD ? g.k : g.n;
   const int64_t ldb = g.k;
 
-  // a thread's rows 4 NTM h + 4 tm .., its columns 4 NTN h + 4 tn ..
   const int tm = tid / NTN, tn = tid % NTN;
-  uint64_t acc[4 * C::RM][2 * C::CN];
+  constexpr int NACC = MODE == GMM_FWD ? C::Q : C::Q / 2;
+  uint64_t acc[C::R][NACC];
 #pragma unroll
-  for (int i = 0; i < 4 * C::RM; ++i)
+  for (int q = 0; q < C::R; ++q)
 #pragma unroll
-    for (int j = 0; j < 2 * C::CN; ++j) acc[i][j] = 0;
+    for (int j = 0; j < NACC; ++j) acc[q][j] = 0;
 
   // a tile of at most half its rows multiplies no others
-  const bool half = MODE != GMM_DW && C::RM > 1 && NI - i0 <= GM / 2;
+  const bool half = MODE != GMM_DW && C::R > 4 && NI - i0 <= GM / 2;
+  // Slice kb is multiplied after a barrier that follows its arrival. By then
+  // the copies of slice kb + 2 are asked for (into the place of slice kb - 1,
+  // which the barrier says is done with) and the loads of slice kb + 1, which
+  // is stored after the products.
   SA sa;
   SB sb;
   const int nk = (int)ceil_div<int64_t>(NT, GK);
-  if (nk > 0) {
-    sa.load(A, lda, i0, NI, 0, NT);
-    sb.load(B, ldb, j0, NJ, 0, NT);
-    sa.store(As[0]);
-    sb.store(Bs[0]);
-    __syncthreads();
+  sa.load(A, lda, i0, NI, 0, NT);
+  sb.load(B, ldb, j0, NJ, 0, NT);
+#pragma unroll
+  for (int p = 0; p < NS - 1; ++p) {
+    SA::copy(As[p], A, lda, i0, NI, p * GK, NT);
+    SB::copy(Bs[p], B, ldb, j0, NJ, p * GK, NT);
+    asm volatile("cp.async.commit_group;" ::: "memory");
   }
+  sa.store(As[0]);
+  sb.store(Bs[0]);
+  int cur = 0;
   for (int kb = 0; kb < nk; ++kb) {
-    const int cur = kb & 1;
-    if (kb + 1 < nk) {
-      sa.load(A, lda, i0, NI, (kb + 1) * GK, NT);
-      sb.load(B, ldb, j0, NJ, (kb + 1) * GK, NT);
-    }
-    if (half) multiply<C, C::RM / 2>(acc, As[cur], Bs[cur], tm, tn);
-    else multiply<C, C::RM>(acc, As[cur], Bs[cur], tm, tn);
-    if (kb + 1 < nk) {
-      sa.store(As[cur ^ 1]);
-      sb.store(Bs[cur ^ 1]);
-      __syncthreads();
-    }
+    asm volatile("cp.async.wait_group %0;" ::"n"(NS - 2) : "memory");
+    __syncthreads();
+    const int nxt = cur + 1 == NS ? 0 : cur + 1, far = cur == 0 ? NS - 1 : cur - 1;
+    const int t1 = (kb + 1) * GK;
+    SA::copy(As[far], A, lda, i0, NI, t1 + GK, NT);
+    SB::copy(Bs[far], B, ldb, j0, NJ, t1 + GK, NT);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    sa.load(A, lda, i0, NI, t1, NT);
+    sb.load(B, ldb, j0, NJ, t1, NT);
+    if (half) multiply<MODE, C, (C::R > 4 ? C::R / 2 : C::R), SA, SB>(acc, As[cur], Bs[cur], tm, tn);
+    else multiply<MODE, C, C::R, SA, SB>(acc, As[cur], Bs[cur], tm, tn);
+    sa.store(As[nxt]);
+    sb.store(Bs[nxt]);
+    cur = nxt;
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
 
-  // rows i and columns j of the tile, four columns at a time (NJ is a
-  // multiple of 4)
   TO* out = static_cast<TO*>(g.out);
   const bool acc_in = MODE == GMM_DW && g.accumulate;
   if (acc_in && sp.count == 0) return;
 #pragma unroll
-  for (int i = 0; i < 4 * C::RM; ++i) {
-    const int ii = i0 + (i / 4) * 4 * NTM + tm * 4 + i % 4;
-    if (ii >= NI) continue;
-    const int64_t row = MODE == GMM_DW ? (int64_t)e * g.n + ii : (int64_t)sp.b + ii;
+  for (int q = 0; q < C::R; ++q) {
+    const int i = i0 + owned<MODE != GMM_DW, NTM>(q, tm);
+    if (i >= NI) continue;
+    TO* o = out + (MODE == GMM_DW ? (int64_t)e * g.n + i : (int64_t)sp.b + i) * NJ;
+    const float* f = reinterpret_cast<const float*>(acc[q]);
+    if (MODE == GMM_FWD) {
 #pragma unroll
-    for (int h = 0; h < C::CN; ++h) {
-      const int j = j0 + h * 4 * NTN + tn * 4;
-      if (j >= NJ) continue;
-      TO* o = out + row * NJ + j;
-      const float* f = reinterpret_cast<const float*>(&acc[i][2 * h]);
-      float4 v = make_float4(f[0], f[1], f[2], f[3]);
-      if (acc_in) {
-        const float4 old = load4<TO>(o);
-        v = make_float4(old.x + v.x, old.y + v.y, old.z + v.z, old.w + v.w);
+      for (int c = 0; c < C::Q; ++c) {
+        const int j = j0 + owned<true, NTN>(c, tn);
+        if (j < NJ) o[j] = from_f32<TO>(f[2 * c] + f[2 * c + 1]);
       }
-      if (sizeof(TO) == 4) {
-        *reinterpret_cast<float4*>(o) = v;
-      } else {
-        const __nv_bfloat162 p0 = __floats2bfloat162_rn(v.x, v.y), p1 = __floats2bfloat162_rn(v.z, v.w);
-        *reinterpret_cast<uint2*>(o) = make_uint2(*reinterpret_cast<const uint32_t*>(&p0),
-                                                  *reinterpret_cast<const uint32_t*>(&p1));
+    } else {
+      // four columns at a time (NJ is a multiple of 4)
+#pragma unroll
+      for (int h = 0; h < C::Q / 4; ++h) {
+        const int j = j0 + owned<false, NTN>(4 * h, tn);
+        if (j >= NJ) continue;
+        float4 v = make_float4(f[4 * h], f[4 * h + 1], f[4 * h + 2], f[4 * h + 3]);
+        if (acc_in) {
+          const float4 old = load4<TO>(o + j);
+          v = make_float4(old.x + v.x, old.y + v.y, old.z + v.z, old.w + v.w);
+        }
+        if (sizeof(TO) == 4) {
+          *reinterpret_cast<float4*>(o + j) = v;
+        } else {
+          const __nv_bfloat162 p0 = __floats2bfloat162_rn(v.x, v.y), p1 = __floats2bfloat162_rn(v.z, v.w);
+          *reinterpret_cast<uint2*>(o + j) = make_uint2(*reinterpret_cast<const uint32_t*>(&p0),
+                                                        *reinterpret_cast<const uint32_t*>(&p1));
+        }
       }
     }
   }
@@ -273,7 +334,12 @@ int64_t ctas_of(int mode, const GmmArgs& g) {
 
 template <typename T, typename TO, int MODE>
 cudaError_t launch(const GmmArgs& g, int num_sms, cudaStream_t st) {
-  const bool small = ctas_of<Large>(MODE, g) <= num_sms;
+  // Small tiles fill the GPU sooner; large ones read shared memory less. Small
+  // against large, us, by the large tiles: products and dx 288: 71 / 104 and
+  // 74 / 95; 640: 70 / 75 and 73 / 82; 768 (few rows an expert): 87 / 116;
+  // 1343: 542 / 556; 2176: 862 / 803; 2607 (dx): 533 / 415. dw, whose count is
+  // exact: 256: 15.4 / 15.6; 512: 15.9 / 14.3; 2048: 35 / 20.
+  const bool small = ctas_of<Large>(MODE, g) <= (int64_t)num_sms * (MODE == GMM_DW ? 2 : 8);
   const int64_t ctas = small ? ctas_of<Small>(MODE, g) : ctas_of<Large>(MODE, g);
   if (ctas == 0) return cudaSuccess;
   if (ctas > INT32_MAX) return cudaErrorInvalidValue;
