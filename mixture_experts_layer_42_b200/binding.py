@@ -304,6 +304,8 @@ def _args(stream, ws: torch.Tensor, *tensors) -> list:
     pointer and size and the stream: the given one, or the current one of the
     workspace's device. All must live there."""
     dev = ws.device
+    if dev.type != "cuda":
+        raise ValueError("tensors passed to libmoe must be on a GPU")
     out = []
     for t in tensors:
         if t is None:

@@ -173,6 +173,15 @@ def test_binding_checks_shapes(M):
         lambda: M.moe_grouped_matvec_w4(z(4, 64), None, off, q.to(torch.int8), s, z(4, 8), ws),
         lambda: M.moe_grouped_swiglu_w4(z(4, 64), None, off, q, s, z(2, 16, 32, dtype=torch.uint8), s, z(4, 8), ws),
     ]
+    # right shapes, but on the host
+    bad += [
+        lambda: M.moe_grouped_matmul(z(4, 24), off, w, z(4, 16), ws),
+        lambda: M.moe_grouped_matmul_dx(z(4, 16), off, w, z(4, 24), ws),
+        lambda: M.moe_grouped_matmul_dw(z(4, 16), z(4, 24), off, w, ws),
+        lambda: M.moe_quantize_w4(z(2, 8, 64), 32, q, s),
+        lambda: M.moe_grouped_matvec_w4(z(4, 64), None, off, q, s, z(4, 8), ws),
+        lambda: M.moe_grouped_swiglu_w4(z(4, 64), None, off, q, s, q, s, z(4, 8), ws),
+    ]
     for i, f in enumerate(bad):
         with pytest.raises(ValueError):
             f()
