@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(GTHREADS, MODE == GMM_FWD ? C::CTAS_FWD : C::C
     for (int j = 0; j < NACC; ++j) acc[q][j] = 0;
 
   // a tile of at most half its rows multiplies no others
-  const bool half = MODE != GMM_DW && C::R > 4 && NI - i0 <= GM / 2;
+  const bool half = C::R > 4 && NI - i0 <= GM / 2;
   // Slice kb is multiplied after a barrier that follows its arrival. By then
   // the copies of slice kb + 2 are asked for (into the place of slice kb - 1,
   // which the barrier says is done with) and the loads of slice kb + 1, which
