@@ -617,26 +617,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     if (MODE != GMM_DW) {
       const int per = (E + 31) / 32;
       int maxc = 0;
+      int64_t wide = 0;             // rows of experts with more than a half's
       int tl[5] = {0, 0, 0, 0, 0};  // tiles at a cap of 512, 256, 128, 64, 32 rows
       for (int u = 0; u < per; ++u) {
         const int e = lane * per + u;
         if (e < E) {
           maxc = max(maxc, cnt[e]);
           rows += cnt[e];
+          if (cnt[e] > MAXN) wide += cnt[e];
 #pragma unroll
           for (int c = 0; c < 5; ++c) tl[c] += (int)(((int64_t)cnt[e] + (512 >> c) - 1) >> (9 - c));
         }
       }
-      // The rows a tile may hold. What bounds large calls is the traffic from
-      // L2, 256 + rows per tile and 64 of the reduction, shared by the pairs;
-      // a small call also waits for its last tile, up to 256 + cap (against
-      // 512 always: 8192 rows of 8 experts of 1024 x 2048 34 instead of 50 us,
-      // 300 rows of one 2048 x 2048 17 instead of 21; 15.4 instead of 14.9 for
-      // 2048 rows of 16 of 1024 x 1024).
+      // The rows a tile may hold, by the time it takes in units of a row or
+      // feature in a step of 64 of the reduction (0.86 ns: the traffic from L2
+      // that the pairs share): (256 + rows) steps and 700 a tile. The write-out
+      // is 14 a row and 200 a tile beside the next tile's MMAs, or 16 a row after its own where
+      // a tile of two halves holds both accumulators. A small call also waits
+      // for its last tile. Against 512 rows always: 8192 rows of 8 experts of
+      // 1024 x 2048 34 instead of 50 us, 16384 of 8 of 4096 x 512 66 instead of
+      // 87, 300 of one 2048 x 2048 17 instead of 21; against 256 always: 65536
+      // of 256 of 2048 x 7168 1814 instead of 2010.
+      const int steps = ((MODE == GMM_FWD ? g.k : g.n) + BK - 1) / BK;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) {
         maxc = max(maxc, __shfl_xor_sync(0xffffffffu, maxc, o));
         rows += __shfl_xor_sync(0xffffffffu, rows, o);
+        wide += __shfl_xor_sync(0xffffffffu, wide, o);
 #pragma unroll
         for (int c = 0; c < 5; ++c) tl[c] += __shfl_xor_sync(0xffffffffu, tl[c], o);
       }
@@ -644,8 +651,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       int64_t best = INT64_MAX;
 #pragma unroll
       for (int c = 0; c < 5; ++c) {
-        const int most = 256 + min(512 >> c, round32(maxc));
-        const int64_t all = ((int64_t)tl[c] * 256 + rows) * nf / npairs;
+        const int m = min(512 >> c, round32(maxc));
+        const int64_t most = (int64_t)(256 + m) * steps + 16 * m;
+        int64_t all = ((int64_t)tl[c] * 256 + rows) * steps + (int64_t)tl[c] * 700;
+        if (c == 0) all += 16 * wide;
+        all = max(all, 14 * rows + (int64_t)tl[c] * 200) * nf / npairs;
         const int64_t cost = tl[c] * (int64_t)nf <= npairs ? most : all + most;
         if (cost < best) { best = cost; cap = 512 >> c; }
       }
