@@ -28,7 +28,7 @@ constexpr int GTHREADS = 64;
 // A tile of M x N by 64 threads, each R rows x Q columns, in slices of K of the
 // reduction, CTAS blocks per SM. What bounds large calls is the fma pipe, with
 // few warps to hide its latency, and the last wave of tiles. 4084 skewed rows
-// of 16 experts of 1032 x 2052: dx 415 us, dw 377 us (46 of the pipe's 74 TF),
+// of 16 experts of 1032 x 2052: dx 415 us, dw 374 us (46 of the pipe's 74 TF),
 // the product 556 us; tiles of 64 x 128 with 16 x 8 a thread (two warps a
 // scheduler) and transposed slices took 442, 398 and 760 us. More blocks an SM
 // spill (the product with 5: 997 us). Calls of few such tiles take small ones,
