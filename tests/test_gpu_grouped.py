@@ -161,6 +161,25 @@ def test_layer_sizes():
         p.check(op, p.run(op))
 
 
+@pytest.mark.parametrize("dtype,on", [(F32, "simt"), (BF, "simt"), (BF, "auto")])
+@pytest.mark.parametrize("op,n,k", [("fwd", 2056, 264), ("dx", 264, 2056), ("dw", 520, 1032), ("dw", 1032, 1288)])
+def test_calls_of_many_tiles(op, n, k, dtype, on):
+    # enough tiles for the large ones of either kernel, and for dw's widths of
+    # 128 (520 x 1032) and 256 inputs
+    counts = [700, 0, 33, 1300, 65] if op != "dw" else [0, 150, 33] * 20 + [65] * 2 if n == 520 else [320] * 23 + [1]
+    M.moe_select_expert_kernel(M.MOE_EXPERT_KERNEL_SIMT if on == "simt" else M.MOE_EXPERT_KERNEL_AUTO)
+    try:
+        p = Problem(counts, n, k, dtype, lead=1, tail=2, seed=n)
+        p.check(op, p.run(op))
+        if op == "dw":
+            base = torch.randn(p.E, n, k, device="cuda", generator=torch.Generator("cuda").manual_seed(4)).to(dtype)
+            out = base.clone()
+            M.moe_grouped_matmul_dw(p.dy, p.x, p.offsets, out, p.ws, accumulate=True)
+            p.check(op, out, base)
+    finally:
+        M.moe_select_expert_kernel(M.MOE_EXPERT_KERNEL_AUTO)
+
+
 def test_rows_past_two_to_the_31_elements():
     # 300k rows of 7168: element offsets pass 2^31; the last rows are right
     k, n, R = 7168, 64, 310_000

@@ -139,6 +139,7 @@ COUNTS = {
     "one_row": [1],
     "few": [0, 1, 2, 3, 4, 5, 0, 6, 7, 8, 9, 0],
     "edges": [15, 16, 17, 31, 32, 33, 0, 40],
+    "mid": [16, 9, 1, 8, 0, 17, 5],
     "many": [65, 0, 130, 1],
     "sparse": [0] * 60 + [1] + [0] * 30 + [2],
 }
