@@ -303,9 +303,9 @@ def _args(stream, ws: torch.Tensor, *tensors) -> list:
     """Device pointers of the (contiguous) tensors or None, then the workspace's
     pointer and size and the stream: the given one, or the current one of the
     workspace's device. All must live there."""
-    dev = ws.device
-    if dev.type != "cuda":
+    if not ws.is_cuda:
         raise ValueError("tensors passed to libmoe must be on a GPU")
+    dev = ws.device
     out = []
     for t in tensors:
         if t is None:
@@ -318,7 +318,7 @@ def _args(stream, ws: torch.Tensor, *tensors) -> list:
         out.append(t.data_ptr())
     if not ws.is_contiguous():
         raise ValueError("tensors passed to libmoe must be contiguous")
-    out += [ws.data_ptr(), ws.numel() * ws.element_size(), _raw_stream(stream, dev)]
+    out += [ws.data_ptr(), ws.nbytes, _current_raw(dev.index) if stream is None else _raw_stream(stream)]
     return out
 
 
@@ -328,10 +328,8 @@ _current_raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _raw_stream(stream, device: torch.device):
-    if stream is not None:
-        return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
-    return _current_raw(device.index) if device.type == "cuda" else None
+def _raw_stream(stream) -> int:
+    return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
 _DT = {torch.float32: MOE_DT_F32, torch.bfloat16: MOE_DT_BF16}
