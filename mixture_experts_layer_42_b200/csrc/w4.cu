@@ -110,7 +110,9 @@ constexpr int MAX_E = 1024;
 
 // TOK = 8 NT token rows a tile; a stage's scales are [KS / group][128] bf16.
 // DEEP: a launch whose tiles are at most two per SM keeps more stages in
-// flight instead of a third tile (one token's up-projection: 43 -> 37 us).
+// flight instead of a third tile (256 tiles of one token's up-projection 37
+// against 42 us; 448 tiles of its down-projection 23.0 against 22.5, 14336 of a
+// decode batch's 451 against 417).
 template <int NT, bool G32, bool DEEP> struct W4Cfg {
   static constexpr int TOK = 8 * NT;
   static constexpr int X_BYTES = TOK * KS * 2;  // 4 slices of [TOK][64]
