@@ -544,12 +544,14 @@ template <bool SWIGLU>
 cudaError_t launch_w4_tokens(const W4Args& g, const W4Tma& m, int64_t bound, int num_sms, cudaStream_t st) {
   // Token rows per tile, by the rows an expert has on average: more rows share
   // their weights' way to operands, fewer leave less padding and more stages.
-  // Down-projection of 256 experts of 7168 x 2048 with 8 / 16 / 32: 417 / 440 /
-  // 451 us at 4 rows, 450 / 464 / 477 at 5, 493 / 485 / 496 at 6, 700 / 573 /
-  // 577 at 10, 811 / 659 / 620 at 12.
+  // Down-projection of 256 experts of 7168 x 2048 with 8 / 16 / 32, uniform
+  // routing: 417 / 440 / 451 us at 4 rows, 450 / 464 / 477 at 5, 493 / 485 /
+  // 496 at 6, 700 / 573 / 577 at 10, 811 / 659 / 620 at 12. Skewed routing
+  // (Zipf 0.6, 1.2) wants more rows sooner, 8 / 16: 331 / 348 and 260 / 254 at
+  // 2, 439 / 440 and 405 / 395 at 4, 483 / 475 and 454 / 426 at 5.
   const int64_t avg = g.rows / g.E;
   if (avg > 10) return launch_w4_group<SWIGLU, 4, false>(g, m, bound, num_sms, st);
-  if (avg > 5) return launch_w4_group<SWIGLU, 2, false>(g, m, bound, num_sms, st);
+  if (avg > 4) return launch_w4_group<SWIGLU, 2, false>(g, m, bound, num_sms, st);
   if (bound <= 2 * (int64_t)num_sms) return launch_w4_group<SWIGLU, 1, true>(g, m, bound, num_sms, st);
   return launch_w4_group<SWIGLU, 1, false>(g, m, bound, num_sms, st);
 }
