@@ -22,6 +22,15 @@ constexpr size_t kWsAlign = 256;
 
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
+// TMA maps in a workspace: 128 bytes each, and at a multiple of 128 in memory,
+// while the workspace itself may begin at any multiple of 16. So their region
+// holds kMapSlack bytes more, and begins where map_region says.
+constexpr size_t kMapBytes = 128;
+constexpr size_t kMapSlack = kMapBytes - 16;
+inline void* map_region(void* ws, size_t off) {
+  return reinterpret_cast<void*>(align_up(reinterpret_cast<uintptr_t>(ws) + off, kMapBytes));
+}
+
 template <typename T>
 __host__ __device__ inline T ceil_div(T a, T b) { return (a + b - 1) / b; }
 

@@ -13,7 +13,7 @@ namespace {
 // Workspace of the grouped products: the error word, then the per-expert maps.
 struct GroupedLayout {
   size_t header;
-  size_t maps;  // [2, E] TMA maps (128 B)
+  size_t maps;  // (map_region) [2, E] TMA maps
   size_t total;
 };
 
@@ -21,7 +21,7 @@ GroupedLayout grouped_layout(int64_t E) {
   GroupedLayout L;
   L.header = 0;
   L.maps = kWsAlign;
-  L.total = align_up(L.maps + (size_t)2 * E * 128, kWsAlign);
+  L.total = align_up(L.maps + (size_t)2 * E * kMapBytes + kMapSlack, kWsAlign);
   return L;
 }
 
@@ -69,7 +69,7 @@ moe_status run_gmm(int mode, const moe_grouped_shape* g, const void* a, const in
   p.err = at<uint32_t>(ws, 0);
   const bool bf16 = g->dtype == MOE_DT_BF16;
   if (bf16 && !simt_selected())
-    return cuda_status(launch_gmm_tc(mode, p, at<void>(ws, grouped_layout(g->n_experts).maps),
+    return cuda_status(launch_gmm_tc(mode, p, map_region(ws, grouped_layout(g->n_experts).maps),
                                      num_sms_current(), s));
   return cuda_status(launch_gmm_simt(mode, bf16, p, num_sms_current(), s));
 }

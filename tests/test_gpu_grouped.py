@@ -361,3 +361,17 @@ def test_gradients_against_differences():
         want = (dw.double() * d.double()).sum().item()
         got = (f(p.x, p.w + d) - f(p.x, p.w - d)) / 2
         assert abs(got - want) <= 1e-4 * (dw.double() * d.double()).abs().sum().item()
+
+
+@pytest.mark.parametrize("at", [16, 32, 64, 112, 240])
+def test_workspace_at_any_multiple_of_16_bytes(at):
+    # dw's maps lie in the workspace: sliced out of a larger tensor, as a pool does
+    p = Problem([40, 0, 129, 7, 300], 264, 520, BF, lead=1, tail=2, seed=17)
+    n = p.ws.numel()
+    pool = torch.full((n + 512,), 0xff, dtype=torch.uint8, device="cuda")
+    p.ws = pool[at:at + n]
+    assert p.ws.data_ptr() % 256 == at
+    M.moe_workspace_init(p.ws)
+    for op in ("fwd", "dx", "dw"):
+        p.check(op, p.run(op))
+    assert bool((pool[:at] == 0xff).all()) and bool((pool[at + n:] == 0xff).all())

@@ -186,3 +186,13 @@ def test_binding_checks_shapes(M):
         with pytest.raises(ValueError):
             f()
             pytest.fail(f"call {i} was taken")
+
+
+@pytest.mark.parametrize("E", [1, 7, 8, 1024])
+def test_workspace_holds_aligned_maps(M, E):
+    # a workspace may begin at any multiple of 16 bytes; the 2 E maps of 128
+    # bytes after its header begin at a multiple of 128
+    n = size(M, n_experts=E)[1]
+    for ws in range(0x10000, 0x10000 + 256, 16):
+        first = -(-(ws + 256) // 128) * 128
+        assert first + 2 * E * 128 <= ws + n
