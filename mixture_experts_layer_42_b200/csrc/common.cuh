@@ -62,7 +62,7 @@ struct WsLayout {
   size_t s;             // [T, D] act
   size_t h;             // [T * k, I] act
   size_t hs;            // [T, I_s] act
-  size_t row_maps;      // [2, E] TMA maps (128 B): A rows of each expert (up, down),
+  size_t row_maps;      // (map_region) [2, E] TMA maps: A rows of each expert (up, down),
                         // then the tile counters of the up and down launches, 64 B apart
   size_t total;
   int router_splits;
@@ -153,7 +153,7 @@ inline WsLayout ws_layout(const moe_config& c, int64_t T) {
   L.s = take((size_t)T * D * ab);
   L.h = take((size_t)T * k * I * ab);
   L.hs = take((size_t)T * (Is > 0 ? Is : 1) * ab);
-  L.row_maps = take((size_t)2 * E * 128 + 128);
+  L.row_maps = take((size_t)2 * E * kMapBytes + 128 + kMapSlack);
   L.total = off;
   return L;
 }

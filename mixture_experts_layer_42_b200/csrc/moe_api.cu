@@ -330,7 +330,7 @@ moe_status moe_experts_grouped(const moe_config* cfg, int64_t T, const void* x_p
   if ((st = check_ws(*cfg, T, ws, ws_bytes, &L)) != MOE_OK) return st;
   if ((st = bind_device((cudaStream_t)stream, ws)) != MOE_OK) return st;
   return run_experts(*cfg, T, x_perm, nullptr, offsets, w1, w3, w2, x, ws1, ws3, ws2, y_perm, s,
-                     at<void>(ws, L.h), at<void>(ws, L.hs), at<void>(ws, L.row_maps),
+                     at<void>(ws, L.h), at<void>(ws, L.hs), map_region(ws, L.row_maps),
                      at<uint32_t>(ws, L.header), (cudaStream_t)stream);
 }
 
@@ -353,7 +353,7 @@ moe_status moe_experts_grouped_gather(const moe_config* cfg, int64_t T, const vo
   if ((st = check_ws(*cfg, T, ws, ws_bytes, &L)) != MOE_OK) return st;
   if ((st = bind_device((cudaStream_t)stream, ws)) != MOE_OK) return st;
   return run_experts(*cfg, T, nullptr, src, offsets, w1, w3, w2, x, ws1, ws3, ws2, y_perm, s,
-                     at<void>(ws, L.h), at<void>(ws, L.hs), at<void>(ws, L.row_maps),
+                     at<void>(ws, L.h), at<void>(ws, L.hs), map_region(ws, L.row_maps),
                      at<uint32_t>(ws, L.header), (cudaStream_t)stream);
 }
 
@@ -437,7 +437,7 @@ moe_status moe_forward(const moe_config* cfg, int64_t T, const void* x, const vo
   void* sbuf = sh ? at<void>(ws, L.s) : nullptr;
   st = run_experts(c, T, x_perm, src, offsets, w1, w3, w2, x, ws1, ws3, ws2,
                    at<void>(ws, L.y_perm), sbuf, at<void>(ws, L.h), at<void>(ws, L.hs),
-                   at<void>(ws, L.row_maps), err, s, small ? nullptr : &place, true);
+                   map_region(ws, L.row_maps), err, s, small ? nullptr : &place, true);
   if (st != MOE_OK) return st;
   return cuda_status(launch_combine(c, T, at<void>(ws, L.y_perm), pos, weights, sbuf, y, s));
 }
@@ -509,7 +509,7 @@ moe_status moe_forward_ep(const moe_config* cfg, int64_t T, int32_t expert_begin
   void* sbuf = shared_local > 0 ? at<void>(ws, L.s) : nullptr;
   st = run_experts(lc, T, x_perm, src, off_local, w1, w3, w2, x, ws1, ws3, ws2,
                    at<void>(ws, L.y_perm), sbuf, at<void>(ws, L.h), at<void>(ws, L.hs),
-                   at<void>(ws, L.row_maps), err, s, small ? nullptr : &place, true);
+                   map_region(ws, L.row_maps), err, s, small ? nullptr : &place, true);
   if (st != MOE_OK) return st;
   return cuda_status(launch_combine_partial(c, T, at<void>(ws, L.y_perm), pos, weights, sbuf,
                                             off_local, lc.n_routed, y_partial, s));
@@ -597,7 +597,7 @@ moe_status moe_forward_fp8(const moe_config* cfg, int64_t T, const void* x, cons
   uint8_t* xq = at<uint8_t>(ws, F.xq);
   float* xs = at<float>(ws, F.xs);
   uint8_t* xq_perm = on_m ? at<uint8_t>(ws, F.xq_perm) : nullptr;
-  void* row_maps = at<void>(ws, L.row_maps);
+  void* row_maps = map_region(ws, L.row_maps);
   if (on_m) {
     // per-expert maps over the routed rows of x and h (the tile counter the
     // kernel also zeroes is not used on this path)

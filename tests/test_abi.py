@@ -155,3 +155,23 @@ def test_launch_count(M):
     finally:
         M.moe_select_expert_kernel(M.MOE_EXPERT_KERNEL_AUTO)
     assert M.moe_forward_launch_count(inputs.CONFIGS["v3_decode"], 0) == -1
+
+
+@pytest.mark.parametrize("E,k,T", [(16, 4, 64), (24, 4, 1), (256, 8, 500)])
+def test_layer_workspace_holds_aligned_maps(M, E, k, T):
+    # a workspace may begin at any multiple of 16 bytes; its last region holds
+    # 2 E maps of 128 bytes, at a multiple of 128, and 128 bytes of counters.
+    # dim 128: the router's reduction is not split
+    D, I = 128, 64
+    cfg = _cfg(n_routed=E, topk=k, n_groups=1, topk_groups=1, dim=D, moe_inter=I, shared_inter=I)
+    n = ctypes.c_size_t(0)
+    assert M.raw_status("moe_workspace_size", ctypes.byref(cfg), T, ctypes.byref(n)) == 0
+    chunks = -(-T // 64)
+    regions = [256, T * E * 4, chunks * E * 4, T * k * 4, T * k * 4, T * k * 4, E * 4, (E + 1) * 4, T * k * 4,
+               T * k * 4, T * k * D * 2, T * D * 2, T * k * I * 2, T * I * 2]
+    at = sum(-(-r // 256) * 256 for r in regions)
+    assert n.value >= at + 2 * E * 128 + 128      # (the regions are the library's)
+    assert n.value < at + 2 * E * 128 + 1024
+    for ws in range(0x10000, 0x10000 + 256, 16):
+        first = -(-(ws + at) // 128) * 128
+        assert first + 2 * E * 128 + 128 <= ws + n.value

@@ -267,3 +267,21 @@ def test_fp8_forward_replays_from_a_cuda_graph(form):
         torch.cuda.synchronize()
         assert torch.equal(got, y)
         assert M.moe_check_error(ws) == M.MOE_OK
+
+
+@pytest.mark.parametrize("at", [16, 64, 112])
+def test_workspace_at_any_multiple_of_16_bytes(form, at):
+    # as the bf16 layer's test of the same name, in both forms
+    F = Fp8Layer(Layer(small()))
+    L, cfg = F.L, F.L.cfg
+    ref = F.forward()[0]
+    n = M.moe_workspace_size_fp8(cfg, L.T)
+    pool = torch.full((n + 256,), 0xff, dtype=torch.uint8, device="cuda")
+    ws = pool[at:at + n]
+    assert ws.data_ptr() % 256 == at
+    M.moe_workspace_init(ws)
+    y = torch.full_like(ref, 7.0)
+    M.moe_forward_fp8(cfg, L.x, L.w_r, L.bias, F.fw, y, ws)
+    assert M.moe_check_error(ws) == M.MOE_OK
+    assert torch.equal(y, ref)
+    assert bool((pool[:at] == 0xff).all()) and bool((pool[at + n:] == 0xff).all())

@@ -513,3 +513,23 @@ def test_forward_replays_from_a_cuda_graph():
         torch.cuda.synchronize()
         assert torch.equal(got, y)
         assert M.moe_check_error(ws) == M.MOE_OK
+
+
+@pytest.mark.parametrize("T", [40, 300])
+@pytest.mark.parametrize("at", [16, 64, 112])
+def test_workspace_at_any_multiple_of_16_bytes(at, T):
+    # the per-expert TMA maps lie in the workspace: sliced out of a larger
+    # tensor, as a pool does, it gives the same bits
+    L = Layer(bf16_small(T=T))
+    c = L.cfg
+    ref = L.forward()[0]
+    n = M.moe_workspace_size(c, T)
+    pool = torch.full((n + 256,), 0xff, dtype=torch.uint8, device="cuda")
+    ws = pool[at:at + n]
+    assert ws.data_ptr() % 256 == at
+    M.moe_workspace_init(ws)
+    y = torch.full_like(ref, 7.0)
+    M.moe_forward(c, L.x, L.w_r, L.bias, *L.w, y, ws)
+    assert M.moe_check_error(ws) == M.MOE_OK
+    assert torch.equal(y, ref)
+    assert bool((pool[:at] == 0xff).all()) and bool((pool[at + n:] == 0xff).all())
