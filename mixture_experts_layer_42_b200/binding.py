@@ -80,6 +80,8 @@ class moe_w4_matrix(ctypes.Structure):
 class moe_w4_weights(ctypes.Structure):
     _fields_ = [(n, moe_w4_matrix) for n in ("w1", "w3", "w2", "ws1", "ws3", "ws2")] + [
         ("group", ctypes.c_int32)]
+    shapes = None   # w4_weights(): (E, N, K) of each matrix, or None for one left out
+    device = None   # and where they are
 
 
 class MoEError(RuntimeError):
@@ -468,19 +470,71 @@ def alloc_workspace_w4(cfg, T: int, device="cuda") -> torch.Tensor:
     return ws
 
 
+_W4_NAMES = ("w1", "w3", "w2", "ws1", "ws3", "ws2")
+
+
 def w4_weights(group, w1, w3, w2, ws1=None, ws3=None, ws2=None) -> moe_w4_weights:
-    """The C struct of 4-bit expert weights; each matrix is a pair (codes,
-    scales) of device tensors, kept alive by the caller."""
-    for m in (w1, w3, w2, ws1, ws3, ws2):
-        _need(m is None or all(t.is_contiguous() for t in m), "tensors passed to libmoe must be contiguous")
-    return moe_w4_weights(*[_w4m(*(m or (None, None))) for m in (w1, w3, w2, ws1, ws3, ws2)],
-                          int(group))
+    """The C struct of 4-bit expert weights; each matrix is a pair (codes
+    uint8 [E, N, K / 2], scales bfloat16 [E, K / group, N]; a shared matrix
+    with E = 1 or without that dimension) of tensors on one GPU, kept alive by
+    the caller."""
+    group = int(group)
+    shapes, tensors = {}, []
+    for name, m in zip(_W4_NAMES, (w1, w3, w2, ws1, ws3, ws2)):
+        shapes[name] = None
+        if m is None:
+            _need(name.startswith("ws"), f"{name}: the experts' matrices are needed")
+            continue
+        q, s = m
+        if name.startswith("ws"):
+            q, s = (t.unsqueeze(0) if t.dim() == 2 else t for t in (q, s))
+        _need(q.dim() == 3 and q.dtype == torch.uint8, f"{name}: codes must be uint8 [E, N, K / 2]")
+        E, n, k = q.shape[0], q.shape[1], 2 * q.shape[2]
+        _need(s.dtype == torch.bfloat16 and group > 0 and s.shape == (E, k // group, n) and k % group == 0,
+              f"{name}: scales must be bfloat16 [E, K / group, N]")
+        _need(q.is_contiguous() and s.is_contiguous(), "tensors passed to libmoe must be contiguous")
+        shapes[name] = (E, n, k)
+        tensors += [q, s]
+    _need(all(t.is_cuda for t in tensors), "tensors passed to libmoe must be on a GPU")
+    _need(len({t.device for t in tensors}) == 1, "tensors on two devices")
+    w = moe_w4_weights(*[_w4m(*(m or (None, None))) for m in (w1, w3, w2, ws1, ws3, ws2)], group)
+    w.shapes, w.device = shapes, tensors[0].device
+    return w
+
+
+def _check_w4_layer(c: moe_config, x, w_router, bias, w4, y, weights_out, idx_out) -> None:
+    """The tensors of moe_forward_w4 against the configuration."""
+    dt = torch.bfloat16 if c.dtype == MOE_DT_BF16 else torch.float32
+    E, D, I, Is = c.n_routed, c.dim, c.moe_inter, c.shared_inter
+    _need(x.dim() == 2 and x.shape[1] == D and x.dtype == dt, f"x must be {dt} [T, {D}]")
+    T = x.shape[0]
+
+    def is_(t, name, shape, dtype):
+        _need(t.shape == shape and t.dtype == dtype, f"{name} must be {dtype} {list(shape)}")
+
+    is_(w_router, "w_router", (E, D), dt)
+    is_(y, "y", (T, D), dt)
+    if c.has_bias and bias is not None:
+        is_(bias, "bias", (E,), torch.float32)
+    if weights_out is not None:
+        is_(weights_out, "weights_out", (T, c.topk), torch.float32)
+    if idx_out is not None:
+        is_(idx_out, "idx_out", (T, c.topk), torch.int32)
+    if w4.shapes is None:
+        return
+    want = dict(w1=(E, I, D), w3=(E, I, D), w2=(E, D, I), ws1=(1, Is, D), ws3=(1, Is, D), ws2=(1, D, Is))
+    for name in _W4_NAMES if Is > 0 else _W4_NAMES[:3]:
+        _need(w4.shapes[name] == want[name],
+              f"{name}: 4-bit weights {w4.shapes[name]}, the configuration's are {want[name]}")
 
 
 def moe_forward_w4(cfg, x, w_router, bias, w4: moe_w4_weights, y, ws, weights_out=None, idx_out=None,
                    stream=None) -> None:
+    c = cfg if isinstance(cfg, moe_config) else make_config(cfg)
+    _check_w4_layer(c, x, w_router, bias, w4, y, weights_out, idx_out)
     xp, rp, bp, yp, wp, ip, *rest = _args(stream, ws, x, w_router, bias, y, weights_out, idx_out)
-    _check(_lib.moe_forward_w4(_c(cfg), x.shape[0], xp, rp, bp, w4, yp, wp, ip, *rest), "moe_forward_w4")
+    _need(w4.device is None or w4.device == ws.device, "tensors on two devices")
+    _check(_lib.moe_forward_w4(ctypes.byref(c), x.shape[0], xp, rp, bp, w4, yp, wp, ip, *rest), "moe_forward_w4")
 
 
 def moe_check_error(ws, stream=None) -> int:

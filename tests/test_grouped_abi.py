@@ -196,3 +196,68 @@ def test_workspace_holds_aligned_maps(M, E):
     for ws in range(0x10000, 0x10000 + 256, 16):
         first = -(-(ws + 256) // 128) * 128
         assert first + 2 * E * 128 <= ws + n
+
+
+def w4_tensors(group=64, E=4, D=128, I=64, Is=64):
+    """(codes, scales) of a layer's six matrices, on the host."""
+    z = torch.zeros
+    pair = lambda e, n, k: (z(e, n, k // 2, dtype=torch.uint8), z(e, k // group, n, dtype=torch.bfloat16))
+    return dict(w1=pair(E, I, D), w3=pair(E, I, D), w2=pair(E, D, I), ws1=pair(1, Is, D), ws3=pair(1, Is, D),
+                ws2=pair(1, D, Is))
+
+
+def test_w4_weights_of_host_tensors_are_refused(M):
+    with pytest.raises(ValueError, match="on a GPU"):
+        M.w4_weights(64, **w4_tensors())
+
+
+@pytest.mark.parametrize("name", ["w1", "w2", "ws3"])
+def test_w4_weights_of_other_types_and_shapes_are_refused(M, name):
+    def refused(what, group=64, **kw):
+        with pytest.raises(ValueError, match=what):
+            M.w4_weights(group, **dict(w4_tensors(), **kw))
+
+    q, s = w4_tensors()[name]
+    refused("codes must be uint8", **{name: (q.to(torch.int8), s)})
+    refused("codes must be uint8", **{name: (q.flatten(), s)})
+    refused("scales must be bfloat16", **{name: (q, s.float())})
+    refused("scales must be bfloat16", **{name: (q, s.transpose(1, 2).contiguous())})
+    refused("scales must be bfloat16", **{name: (q[..., :-16].contiguous(), s)})
+    refused("scales must be bfloat16", group=32)
+    refused("scales must be bfloat16", group=0)
+    refused("contiguous", **{name: (q.transpose(0, 1).contiguous().transpose(0, 1) if q.shape[0] > 1 else
+                                    torch.zeros(1, q.shape[1], 2 * q.shape[2], dtype=torch.uint8)[..., ::2], s)})
+    if not name.startswith("ws"):
+        refused("are needed", **{name: None})
+
+
+def test_w4_layer_tensors_are_checked_against_the_configuration(M):
+    cfg = M.moe_config(dim=128, n_routed=4, n_groups=1, topk_groups=1, topk=2, moe_inter=64, shared_inter=64, score=0,
+                       route_scale=1.0, has_bias=1, dtype=1)
+    z = lambda *s, dtype=torch.bfloat16: torch.zeros(*s, dtype=dtype)
+    F = torch.float32
+
+    def weights(**kw):
+        m = M.moe_w4_matrix(0x10000, 0x10000)
+        w = M.moe_w4_weights(m, m, m, m, m, m, 64)
+        w.shapes = dict(dict(w1=(4, 64, 128), w3=(4, 64, 128), w2=(4, 128, 64), ws1=(1, 64, 128), ws3=(1, 64, 128),
+                             ws2=(1, 128, 64)), **kw)
+        return w
+
+    def refused(what, x=z(8, 128), r=z(4, 128), b=z(4, dtype=F), w=None, y=z(8, 128), wo=None, io=None):
+        with pytest.raises(ValueError, match=what):
+            M.moe_forward_w4(cfg, x, r, b, w or weights(), y, z(1 << 16, dtype=torch.uint8), wo, io)
+
+    refused("x must be", x=z(8, 120))
+    refused("x must be", x=z(8, 128, dtype=F))
+    refused("w_router must be", r=z(5, 128))
+    refused("w_router must be", r=z(4, 128, dtype=F))
+    refused("bias must be", b=z(4))
+    refused("y must be", y=z(7, 128))
+    refused("y must be", y=z(8, 128, dtype=F))
+    refused("weights_out must be", wo=z(8, 4, dtype=F))
+    refused("idx_out must be", io=z(8, 2, dtype=torch.int64))
+    for name, shape in (("w1", (4, 64, 64)), ("w3", (3, 64, 128)), ("w2", (4, 64, 128)), ("ws1", (1, 128, 128)),
+                        ("ws2", None)):
+        refused(name + ": 4-bit weights", w=weights(**{name: shape}))
+    refused("on a GPU")                                           # right, but on the host
