@@ -39,8 +39,9 @@
 // counted, and 0.85-1.15 PFLOP/s. A loop of seconds is bound by the 1 kW power
 // cap (65536 rows: 2050-2250 us at 1.1-1.2 GHz). dw tiles of 256 x 512, whose
 // write-out nothing overlaps for want of a second accumulator, took 233 and
-// 653 us; a panel of dy kept over a row of tiles 190 and 757. Every wait is bounded (1 s); on expiry the kernel raises
-// the error word's timeout bit, drains its copies and returns.
+// 653 us; a panel of dy kept over a row of tiles 190 and 757. Every wait is
+// bounded (1 s, in DW and 4 us for each 64 rows of the call); on expiry the
+// kernel raises the error word's timeout bit, drains its copies and returns.
 #include "api_common.cuh"
 #include "gmm.cuh"
 #include "tc_common.cuh"
@@ -63,6 +64,10 @@ constexpr int MAX_E = 1024;
 constexpr int NBOX = 9;                   // row boxes of 8, 16, 32, 48, ... 128 rows
 constexpr int SLOTS = 12;                 // stages in flight, at most
 constexpr int TQ = 4;                     // tiles the scheduler works out ahead
+// DW: what a step of 64 rows adds to the waits' limit. The epilogue waits for
+// a tile's whole reduction, and the scheduler's queue for the epilogue: all rows
+// of an expert, up to 2^30. A step takes 0.1-0.8 us.
+constexpr uint64_t STEP_LIMIT_NS = 4000;
 
 template <int MODE> struct Cfg {
   static constexpr int HALVES = MODE == GMM_DW ? 1 : 2;
@@ -86,6 +91,7 @@ struct TcGmm {
   int nw;                   // DW: inputs per tile
   int wide;                 // MN-major A by one box of 128 features (rows of whole 64s)
   int stall;                // test hook: CTA 0's MMA thread lets a wait run out
+  uint64_t wait_ns;         // limit of each wait
   uint32_t* err;
 };
 
@@ -210,8 +216,9 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 // A wait by the whole warp; all lanes agree on its outcome.
-__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t* err) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, err));
+__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t* err,
+                                         uint64_t limit) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, err, limit));
 }
 
 // A role's place in the scheduler's queue of tiles. next() reads a tile for
@@ -219,8 +226,8 @@ __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatil
 struct TileQueue {
   uint32_t q = 0, ph = 0;
   __device__ __forceinline__ bool next(Tile& t, const Tile* tq, uint64_t* qfull, uint64_t* qempty, int lane,
-                                       volatile int* abort_flag, uint32_t* err) {
-    if (!wait_all(&qfull[q], ph, abort_flag, err)) return false;
+                                       volatile int* abort_flag, uint32_t* err, uint64_t limit) {
+    if (!wait_all(&qfull[q], ph, abort_flag, err, limit)) return false;
     t = uniform(tq[q]);
     if (lane == 0) mbar_arrive(&qempty[q]);
     if (++q == TQ) { q = 0; ph ^= 1; }
@@ -275,8 +282,9 @@ template <int MODE> struct Outstanding {
   uint32_t old_n = 0, old_sz = 0, new_n = 0, new_sz = 0;
   uint32_t pos = 0, v = 0, vpos = 0;  // the oldest's offset and count; the next's count
   uint32_t slot = 0, ph = 0;          // the oldest's barrier
-  __device__ __forceinline__ bool retire(uint64_t* empty, volatile int* abort_flag, uint32_t* err) {
-    if (!wait_all(&empty[slot], ph, abort_flag, err)) return false;
+  __device__ __forceinline__ bool retire(uint64_t* empty, volatile int* abort_flag, uint32_t* err,
+                                         uint64_t limit) {
+    if (!wait_all(&empty[slot], ph, abort_flag, err, limit)) return false;
     if (++slot == SLOTS) { slot = 0; ph ^= 1; }
     pos += old_sz;
     v += old_sz;
@@ -292,16 +300,17 @@ template <int MODE> struct Outstanding {
     return true;
   }
   // before a tile of stages of sz bytes: two runs at most
-  __device__ __forceinline__ bool begin(uint32_t sz, uint64_t* empty, volatile int* abort_flag, uint32_t* err) {
+  __device__ __forceinline__ bool begin(uint32_t sz, uint64_t* empty, volatile int* abort_flag, uint32_t* err,
+                                        uint64_t limit) {
     while (new_n > 0 && new_sz != sz)
-      if (!retire(empty, abort_flag, err)) return false;
+      if (!retire(empty, abort_flag, err, limit)) return false;
     return true;
   }
   // until `bytes` more (padding included) and a slot are free
   __device__ __forceinline__ bool make_room(uint32_t bytes, uint64_t* empty, volatile int* abort_flag,
-                                            uint32_t* err) {
+                                            uint32_t* err, uint64_t limit) {
     while (old_n > 0 && (old_n + new_n == SLOTS || vpos + bytes - v > (uint32_t)Cfg<MODE>::RING))
-      if (!retire(empty, abort_flag, err)) return false;
+      if (!retire(empty, abort_flag, err, limit)) return false;
     return true;
   }
   __device__ __forceinline__ void push(uint32_t sz, uint32_t at, uint32_t pad) {
@@ -486,7 +495,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     bool ok = true;
     TileQueue T;
     Tile t;
-    while (ok && T.next(t, tq, qfull, qempty, lane, abort_flag, g.err)) {
+    while (ok && T.next(t, tq, qfull, qempty, lane, abort_flag, g.err, g.wait_ns)) {
       const int kb_n = (t.depth + BK - 1) / BK;
       if (kb_n == 0) continue;
       const uint32_t sz = stage_bytes<MODE>(t);
@@ -516,10 +525,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         if (t.halves == 2) rows += box_rows(row_box(c1, n1, 0)) + box_rows(row_box(c1, n1, 1));
         tx += (uint32_t)rows * (BK * 2);
       }
-      ok = Q.begin(sz, empty, abort_flag, g.err);
+      ok = Q.begin(sz, empty, abort_flag, g.err, g.wait_ns);
       for (int kb = 0; ok && kb < kb_n; ++kb) {
         const uint32_t at = R.place(sz);
-        if (!Q.make_room(R.pad + sz, empty, abort_flag, g.err)) { ok = false; break; }
+        if (!Q.make_room(R.pad + sz, empty, abort_flag, g.err, g.wait_ns)) { ok = false; break; }
         Q.push(sz, at, R.pad);
         if (el) {
           uint8_t* sa = tiles + at;
@@ -570,10 +579,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       const uint32_t tiles0 = smem_u32(tiles);
       uint32_t hb = 0;  // halves so far; half i uses accumulator i & 1
       bool ok = true;
-      if (g.stall && blockIdx.x == 0) ok = wait_all(drain, 0, abort_flag, g.err);
+      if (g.stall && blockIdx.x == 0) ok = wait_all(drain, 0, abort_flag, g.err, g.wait_ns);
       TileQueue T;
       Tile t;
-      while (ok && T.next(t, tq, qfull, qempty, lane, abort_flag, g.err)) {
+      while (ok && T.next(t, tq, qfull, qempty, lane, abort_flag, g.err, g.wait_ns)) {
         const int kb_n = (t.depth + BK - 1) / BK;
         if (kb_n == 0) continue;
         const uint32_t sz = stage_bytes<MODE>(t), b1 = (uint32_t)half_n(t, 0) * BK;
@@ -581,13 +590,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         const uint32_t id0 = idesc_bf16(2 * FM, half_n(t, 0)) | MAJ;
         const uint32_t id1 = t.halves == 2 ? idesc_bf16(2 * FM, half_n(t, 1)) | MAJ : 0u;
         const uint32_t d0 = tmem_base + (hb & 1) * MAXN, d1 = tmem_base + (~hb & 1) * MAXN;
-        if (!wait_all(&tempty[hb & 1], ((hb >> 1) & 1) ^ 1, abort_flag, g.err)) break;
-        if (t.halves == 2 && !wait_all(&tempty[~hb & 1], (((hb + 1) >> 1) & 1) ^ 1, abort_flag, g.err))
+        if (!wait_all(&tempty[hb & 1], ((hb >> 1) & 1) ^ 1, abort_flag, g.err, g.wait_ns)) break;
+        if (t.halves == 2 && !wait_all(&tempty[~hb & 1], (((hb + 1) >> 1) & 1) ^ 1, abort_flag, g.err, g.wait_ns))
           break;
         tc_fence_after();
         for (int kb = 0; kb < kb_n; ++kb) {
           const uint32_t st = tiles0 + R.place(sz);
-          if (!wait_all(&full[R.slot], R.ph, abort_flag, g.err)) { ok = false; break; }
+          if (!wait_all(&full[R.slot], R.ph, abort_flag, g.err, g.wait_ns)) { ok = false; break; }
           tc_fence_after();
           if (el) {
             const uint32_t al = desc_lo<A_MN>(st), bl = desc_lo<B_MN>(st + TILE);
@@ -700,7 +709,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       Tile t;
       t.e = -1;
       if (i < S.total) t = decode<MODE>(S, i);
-      if (!wait_all(&qempty[q], ph ^ 1, abort_flag, g.err)) break;
+      if (!wait_all(&qempty[q], ph ^ 1, abort_flag, g.err, g.wait_ns)) break;
       if (lane == 0) {
         tq[q] = t;
         mbar_arrive(&qfull[q]);
@@ -717,13 +726,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     int ok = 1;
     TileQueue T;
     Tile t;
-    while (ok && T.next(t, tq, qfull, qempty, lane, abort_flag, g.err)) {
+    while (ok && T.next(t, tq, qfull, qempty, lane, abort_flag, g.err, g.wait_ns)) {
       const int fw = t.f0 + (int)rank * FM + quad * 32;  // this warp's first feature
       const bool zero = t.depth == 0;  // DW of an expert without rows
       if (zero && g.accumulate) continue;
       for (int h = 0; h < t.halves; ++h) {
         if (!zero) {
-          if (lane == 0) ok = mbar_wait(&tfull[hb & 1], (hb >> 1) & 1, abort_flag, g.err) ? 1 : 0;
+          if (lane == 0) ok = mbar_wait(&tfull[hb & 1], (hb >> 1) & 1, abort_flag, g.err, g.wait_ns) ? 1 : 0;
           ok = __shfl_sync(0xffffffffu, ok, 0);
           if (!ok) break;
           tc_fence_after();
@@ -890,6 +899,8 @@ cudaError_t launch(const GmmArgs& a, void* maps, int num_sms, cudaStream_t st) {
   g.out_f32 = a.out_f32;
   g.accumulate = a.accumulate;
   g.stall = pipeline_stall() == STALL_EXPERTS_UP ? 1 : 0;
+  g.wait_ns = WAIT_LIMIT_NS;
+  if (MODE == GMM_DW) g.wait_ns += (uint64_t)ceil_div<int64_t>(a.rows, BK) * STEP_LIMIT_NS;
   g.err = a.err;
   // upper bound on the tiles (the count depends on the device's offsets)
   const int64_t nf = ceil_div(MODE == GMM_DX ? a.k : a.n, 2 * FM);

@@ -12,7 +12,10 @@
 namespace moe {
 namespace tc {
 
-constexpr uint64_t WAIT_LIMIT_NS = 1000000000ull;   // 1 s: no legitimate wait comes close
+// 1 s. A wait is for one stage, or for one tile: of the layer's kernels, of at
+// most 2^20 inputs, milliseconds. A kernel whose tiles may be longer passes its
+// own limit (dw of the grouped products, over all rows of an expert).
+constexpr uint64_t WAIT_LIMIT_NS = 1000000000ull;
 constexpr uint64_t DRAIN_LIMIT_NS = 20000000ull;    // 20 ms, only while draining after an abort
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
@@ -64,16 +67,17 @@ __device__ __forceinline__ bool mbar_try_wait_sleep(uint64_t* bar, uint32_t pari
 }
 
 // Slow path of mbar_wait: poll with sleeping try_waits, giving up when
-// another role has raised the abort flag or after WAIT_LIMIT_NS (then raises
-// it); both are checked every 64 polls.
+// another role has raised the abort flag or after limit_ns (then raises it);
+// both are checked every 64 polls.
 static __device__ __noinline__ bool mbar_wait_slow(uint64_t* bar, uint32_t parity,
-                                                   volatile int* abort_flag, uint32_t* err) {
+                                                   volatile int* abort_flag, uint32_t* err,
+                                                   uint64_t limit_ns) {
   const uint64_t t0 = globaltimer();
   for (uint32_t n = 1;; ++n) {
     if (mbar_try_wait_sleep(bar, parity)) return true;
     if ((n & 63) == 0) {
       if (*abort_flag) return false;
-      if (globaltimer() - t0 > WAIT_LIMIT_NS) {
+      if (globaltimer() - t0 > limit_ns) {
         *abort_flag = 1;
         set_error(err, ERRBIT_TIMEOUT);
         return false;
@@ -86,9 +90,9 @@ static __device__ __noinline__ bool mbar_wait_slow(uint64_t* bar, uint32_t parit
 // mbar_wait_slow). The first try is inline: on the pipeline's critical path
 // the phase has usually completed already.
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
-                                          uint32_t* err) {
+                                          uint32_t* err, uint64_t limit_ns = WAIT_LIMIT_NS) {
   if (mbar_try_wait(bar, parity)) return true;
-  return mbar_wait_slow(bar, parity, abort_flag, err);
+  return mbar_wait_slow(bar, parity, abort_flag, err, limit_ns);
 }
 
 // Bounded wait used only while draining after an abort.

@@ -375,3 +375,22 @@ def test_workspace_at_any_multiple_of_16_bytes(at):
     for op in ("fwd", "dx", "dw"):
         p.check(op, p.run(op))
     assert bool((pool[:at] == 0xff).all()) and bool((pool[at + n:] == 0xff).all())
+
+
+def test_dw_of_more_rows_than_a_second_reads():
+    # one expert of 2^30 rows, the most there may be: one tile, whose reduction
+    # takes longer than the waits' second. Rows of zeros but for 4000
+    R, n = 1 << 30, 8
+    x = torch.zeros(R, n, dtype=BF, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(18)
+    rows = torch.cat([torch.randint(0, R, (3998,), generator=g, device="cuda"),
+                      torch.tensor([0, R - 1], device="cuda")]).unique()
+    x[rows] = torch.randn(len(rows), n, generator=g, device="cuda").to(BF)
+    off = torch.tensor([0, R], dtype=torch.int32, device="cuda")
+    ws = M.alloc_workspace_grouped(R, 1, n, n, BF)
+    dw = torch.full((1, n, n), 7.0, device="cuda")
+    M.moe_grouped_matmul_dw(x, x, off, dw, ws)
+    assert M.moe_check_error(ws) == M.MOE_OK
+    v = x[rows].double()
+    # (additions of zeros are exact)
+    assert bool(((dw[0].double() - v.T @ v).abs() <= (len(rows) + 2) * 2.0 ** -23 * (v.abs().T @ v.abs())).all())
