@@ -112,15 +112,19 @@ constexpr int MAX_E = 1024;
 // DEEP: a launch whose tiles are at most two per SM keeps more stages in
 // flight instead of a third tile (256 tiles of one token's up-projection 37
 // against 42 us; 448 tiles of its down-projection 23.0 against 22.5, 14336 of a
-// decode batch's 451 against 417).
+// decode batch's 451 against 417). Groups of 32, whose stages are larger, keep
+// four: with five only one block fits an SM, and the second tiles wait (the
+// same up-projection 49.3 against 37.7 us, 41.5 without the deep form).
 template <int NT, bool G32, bool DEEP> struct W4Cfg {
   static constexpr int TOK = 8 * NT;
   static constexpr int X_BYTES = TOK * KS * 2;  // 4 slices of [TOK][64]
   static constexpr int S_BYTES = WR * (KS / (G32 ? 32 : 64)) * 2;
   static constexpr int STAGE_BYTES = W_BYTES + X_BYTES + S_BYTES;
   static constexpr int CTAS = NT == 1 && !DEEP ? 3 : 2;  // per SM
-  static constexpr int STAGES = DEEP ? 5 : NT == 2 ? 4 : 3;
+  static constexpr int STAGES = DEEP ? (G32 ? 4 : 5) : NT == 2 ? 4 : 3;
   static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE_BYTES + 256 + (MAX_E + 1) * 4;
+  // an SM has 228 KB; each block takes 1 KB beside its own
+  static_assert(CTAS * (SMEM + 1024) <= 228 * 1024, "CTAS blocks per SM");
 };
 
 struct W4Tma {
@@ -526,11 +530,17 @@ template <bool SWIGLU, int NT, int GPC, bool DEEP>
 cudaError_t launch_w4_kernel(const W4Args& g, const W4Tma& m, int64_t bound, int num_sms, cudaStream_t st) {
   using C = W4Cfg<NT, GPC == 1, DEEP>;
   static std::atomic<uint64_t> allowed{0};
-  cudaError_t e = allow_smem(w4_kernel<SWIGLU, NT, GPC, DEEP>, (int)C::SMEM, &allowed);
+  // Groups of 32: blocks of at most one tile per SM ask for more than half of
+  // its shared memory, so that no two share an SM while others idle (128 tiles
+  // of 64 outputs, 7168 inputs: 25.4 against 29.2 us a call, back to back).
+  constexpr bool SPREAD = DEEP && GPC == 1;
+  constexpr size_t ALONE = 116 * 1024;
+  const size_t smem = SPREAD && bound <= num_sms ? ALONE : C::SMEM;
+  cudaError_t e = allow_smem(w4_kernel<SWIGLU, NT, GPC, DEEP>, (int)(SPREAD ? ALONE : C::SMEM), &allowed);
   if (e != cudaSuccess) return e;
   const int64_t most = (int64_t)C::CTAS * num_sms;
   return launch_pdl(true, w4_kernel<SWIGLU, NT, GPC, DEEP>, dim3((unsigned)(bound < most ? bound : most)),
-                    dim3(NUM_THREADS), C::SMEM, st, g, m);
+                    dim3(NUM_THREADS), smem, st, g, m);
 }
 
 template <bool SWIGLU, int NT, bool DEEP>

@@ -156,6 +156,16 @@ def test_products(counts, n, k, group, gather, mats):
     p.check()
 
 
+@pytest.mark.parametrize("mats", [1, 2])
+@pytest.mark.parametrize("n", [640, 1280, 2560])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_few_rows_of_many_tiles(group, n, mats):
+    # 60 to 480 tiles of one row: at most one, two and more a multiprocessor
+    p = Problem([1] * 6 + [0] + [1] * 6, n, 1152, group, False, mats, lead=1, tail=1, seed=n + group)
+    p.run()
+    p.check()
+
+
 def test_layer_sizes():
     counts = [0] * 256
     for e in (3, 17, 40, 99, 120, 200, 222, 255):
