@@ -68,6 +68,13 @@ constexpr int TQ = 4;                     // tiles the scheduler works out ahead
 // a tile's whole reduction, and the scheduler's queue for the epilogue: all rows
 // of an expert, up to 2^30. A step takes 0.1-0.8 us.
 constexpr uint64_t STEP_LIMIT_NS = 4000;
+// DW: steps summed in tensor memory, 768 rows. The tensor cores truncate every
+// addition into their fp32 sums, which costs 1.1e-9 of the result a row: of
+// 8192 random rows 9.1e-6, of 2^20 1.2e-3, and of 2^20 positive ones 9e-3.
+// Longer reductions add such parts up in registers, where fp32 additions round:
+// 7e-7 at any length (65536 rows of 8 experts of 2048 x 2048: 410 instead of
+// 395 us; parts of 512 rows 417).
+constexpr int PART = 12;
 
 template <int MODE> struct Cfg {
   static constexpr int HALVES = MODE == GMM_DW ? 1 : 2;
@@ -349,16 +356,53 @@ __device__ __forceinline__ void tmem_ld16x32(uint32_t taddr, uint32_t (&r)[16]) 
       : "r"(taddr));
 }
 
-// 32 outputs x 32 inputs of dw from a warp's registers (tmem_ld16x32 of its
-// lanes 0-15 and 16-31), nr and nc of them valid, added to what is there in
-// fp32 when ACC. Four threads hold 8 neighbouring inputs of a row: 32 bytes of
-// fp32; for bf16 the rounded pairs of two blocks of 8 are exchanged between
-// them, so that four threads write 32 bytes of bf16 too (16-byte pieces of L2's
-// sectors cost the softmax layer's gradient a tenth; exchanging fp32, twice the
-// shuffles, took 172 instead of 137 us of 26 rows' 5744 x 7160 of 6 experts).
-template <bool ACC>
-__device__ __forceinline__ void store_dw(const uint32_t (&r)[2][16], float* out, int64_t ld, int nr, int nc,
-                                         int lane) {
+// A 32 x 32 block of dw (outputs x inputs) lies in a warp's registers as
+// tmem_ld16x32 leaves its lanes 0-15 and 16-31; nr x nc of it are valid. Four
+// threads hold 8 neighbouring inputs of a row, thread t of them 2t and 2t + 1.
+
+__device__ __forceinline__ float2 pair_at(const float* p) { return *reinterpret_cast<const float2*>(p); }
+__device__ __forceinline__ float2 pair_at(const __nv_bfloat16* p) {
+  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(p));
+}
+
+// Brings into L2 what this warp will add of a tile of dw, while it is multiplied:
+// the accumulating 24576 rows of 64 experts of 1408 x 2048 469 instead of 591 us.
+template <typename T>
+__device__ __forceinline__ void prefetch_old(const TcGmm& g, const Tile& t, int fw, int cg, int lane) {
+  if (fw + lane >= g.n) return;
+  const T* row = static_cast<const T*>(g.out) + ((int64_t)t.e * g.n + fw + lane) * g.k + t.c0;
+  for (int c = cg * 32; c < t.cols; c += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + c));
+}
+
+// Adds what dw holds, all of it asked for at once (the same call 591 instead of
+// 721 us with a row of the block asked for, added and stored before the next;
+// 16384 rows of 32 of 2048 x 7168 in fp32 982 instead of 2420).
+template <typename T>
+__device__ __forceinline__ void add_old(float (&r)[2][16], const T* out, int64_t ld, int nr, int nc, int lane) {
+  float2 o[4][4];
+#pragma unroll
+  for (int h = 0; h < 4; ++h) {
+    const int row = h * 8 + (lane >> 2);
+    const T* p = out + (int64_t)row * ld + (lane & 3) * 2;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[h][i] = row < nr && 8 * i < nc ? pair_at(p + 8 * i) : make_float2(0.f, 0.f);
+  }
+#pragma unroll
+  for (int h = 0; h < 4; ++h)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      r[h >> 1][4 * i + (h & 1) * 2] += o[h][i].x;
+      r[h >> 1][4 * i + (h & 1) * 2 + 1] += o[h][i].y;
+    }
+  __syncwarp();  // read before other lanes' stores
+}
+
+// Writes it: 32 bytes of fp32 by four threads; for bf16 the rounded pairs of
+// two blocks of 8 are exchanged between them, so that four threads write 32
+// bytes of bf16 too (16-byte pieces of L2's sectors cost the softmax layer's
+// gradient a tenth; exchanging fp32, twice the shuffles, took 172 instead of
+// 137 us of 26 rows' 5744 x 7160 of 6 experts).
+__device__ __forceinline__ void store_dw(const float (&r)[2][16], float* out, int64_t ld, int nr, int nc, int lane) {
 #pragma unroll
   for (int h = 0; h < 4; ++h) {
     const int row = h * 8 + (lane >> 2);
@@ -366,37 +410,24 @@ __device__ __forceinline__ void store_dw(const uint32_t (&r)[2][16], float* out,
     if (row < nr)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (8 * i < nc) {
-          float2 v = make_float2(__uint_as_float(r[h >> 1][4 * i + (h & 1) * 2]),
-                                 __uint_as_float(r[h >> 1][4 * i + (h & 1) * 2 + 1]));
-          if (ACC) {
-            const float2 o = *reinterpret_cast<const float2*>(p + 8 * i);
-            v = make_float2(o.x + v.x, o.y + v.y);
-          }
-          *reinterpret_cast<float2*>(p + 8 * i) = v;
-        }
+        if (8 * i < nc)
+          *reinterpret_cast<float2*>(p + 8 * i) =
+              make_float2(r[h >> 1][4 * i + (h & 1) * 2], r[h >> 1][4 * i + (h & 1) * 2 + 1]);
   }
 }
-template <bool ACC>
-__device__ __forceinline__ void store_dw(const uint32_t (&r)[2][16], __nv_bfloat16* out, int64_t ld, int nr,
-                                         int nc, int lane) {
+__device__ __forceinline__ void store_dw(const float (&r)[2][16], __nv_bfloat16* out, int64_t ld, int nr, int nc,
+                                         int lane) {
   const int t = lane & 3;
 #pragma unroll
   for (int h = 0; h < 4; ++h) {
     const int row = h * 8 + (lane >> 2);
-    uint32_t w[4];  // this thread's pair of inputs 2 t, 2 t + 1 of each block of 8
+    uint32_t w[4];  // this thread's pair of each block of 8
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float a = __uint_as_float(r[h >> 1][4 * i + (h & 1) * 2]), b = __uint_as_float(r[h >> 1][4 * i + (h & 1) * 2 + 1]);
-      if (ACC && row < nr && 8 * i < nc) {
-        const float2 o = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(out + (int64_t)row * ld + 8 * i + 2 * t));
-        a += o.x;
-        b += o.y;
-      }
-      const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
+      const __nv_bfloat162 p =
+          __floats2bfloat162_rn(r[h >> 1][4 * i + (h & 1) * 2], r[h >> 1][4 * i + (h & 1) * 2 + 1]);
       w[i] = *reinterpret_cast<const uint32_t*>(&p);
     }
-    if (ACC) __syncwarp();  // the old values are read before other lanes' stores
     // threads 0 and 1 take block 2u, threads 2 and 3 block 2u + 1: inputs
     // 4 (t & 1) .. + 3
 #pragma unroll
@@ -410,6 +441,44 @@ __device__ __forceinline__ void store_dw(const uint32_t (&r)[2][16], __nv_bfloat
         *reinterpret_cast<uint2*>(out + (int64_t)row * ld + c) = (t & 1) ? make_uint2(x, hi) : make_uint2(lo, x);
     }
   }
+}
+
+// Into dw, from output fw and the tile's input c on.
+template <typename T>
+__device__ __forceinline__ void put_dw(const TcGmm& g, float (&v)[2][16], const Tile& t, int fw, int c, int lane) {
+  T* out = static_cast<T*>(g.out) + ((int64_t)t.e * g.n + fw) * g.k + t.c0 + c;
+  const int nr = g.n - fw, nc = t.cols - c;
+  if (g.accumulate) add_old(v, out, g.k, nr, nc, lane);
+  store_dw(v, out, g.k, nr, nc, lane);
+}
+
+// mbar_wait without a call.
+__device__ __forceinline__ bool wait_inline(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t* err,
+                                            uint64_t limit) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer();
+  for (uint32_t n = 1; !mbar_try_wait_sleep(bar, parity); ++n) {
+    if ((n & 63) != 0) continue;
+    if (*abort_flag) return false;
+    if (globaltimer() - t0 > limit) {
+      *abort_flag = 1;
+      set_error(err, ERRBIT_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
+
+// 16 TMEM lanes x 16 columns (tmem_ld16x32's first half), and the inverse.
+__device__ __forceinline__ void tmem_ld16x16(uint32_t taddr, float (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st16x16(uint32_t taddr, const float (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.16x256b.x2.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+               "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7])
+               : "memory");
 }
 
 template <int MODE>
@@ -594,18 +663,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         if (t.halves == 2 && !wait_all(&tempty[~hb & 1], (((hb + 1) >> 1) & 1) ^ 1, abort_flag, g.err, g.wait_ns))
           break;
         tc_fence_after();
+        uint32_t dp = d0;  // DW: the part's accumulator
+        bool sum = false;  // added to what it holds
         for (int kb = 0; kb < kb_n; ++kb) {
+          if (MODE == GMM_DW && kb > 0 && kb % PART == 0) {  // the next part, in the other one
+            if (el) commit_pair(&tfull[hb & 1]);
+            ++hb;
+            dp = tmem_base + (hb & 1) * MAXN;
+            sum = false;
+            if (!wait_all(&tempty[hb & 1], ((hb >> 1) & 1) ^ 1, abort_flag, g.err, g.wait_ns)) { ok = false; break; }
+            tc_fence_after();
+          }
           const uint32_t st = tiles0 + R.place(sz);
           if (!wait_all(&full[R.slot], R.ph, abort_flag, g.err, g.wait_ns)) { ok = false; break; }
           tc_fence_after();
           if (el) {
             const uint32_t al = desc_lo<A_MN>(st), bl = desc_lo<B_MN>(st + TILE);
             if (C::HALVES == 2 && t.halves == 2)
-              mma_stage<A_MN, B_MN, true>(d0, d1, al, bl, bl + (b1 >> 4), id0, id1, kb > 0);
+              mma_stage<A_MN, B_MN, true>(d0, d1, al, bl, bl + (b1 >> 4), id0, id1, sum);
             else
-              mma_stage<A_MN, B_MN, false>(d0, 0, al, bl, 0, id0, 0, kb > 0);
+              mma_stage<A_MN, B_MN, false>(dp, 0, al, bl, 0, id0, 0, sum);
             commit_pair(&empty[R.slot]);
           }
+          sum = true;
           R.advance(sz);
         }
         if (!ok) break;
@@ -730,8 +810,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       const int fw = t.f0 + (int)rank * FM + quad * 32;  // this warp's first feature
       const bool zero = t.depth == 0;  // DW of an expert without rows
       if (zero && g.accumulate) continue;
+      if (MODE == GMM_DW && g.accumulate) {
+        if (g.out_f32) prefetch_old<float>(g, t, fw, cg, lane);
+        else prefetch_old<__nv_bfloat16>(g, t, fw, cg, lane);
+      }
+      const bool parts = MODE == GMM_DW && t.depth > PART * BK;
+      if (parts) {
+        // the parts' sums are added up in registers, and the whole is left in
+        // the last part's accumulator, from where it is written out as any
+        // tile (a write-out of its own, from the registers, cost the tiles of
+        // one part 3 %)
+        constexpr int NB = MODE == GMM_DW ? MAXN / 64 : 1;  // this warp's blocks of 32 inputs
+        float sum[NB * 4][8];
+#pragma unroll
+        for (int b = 0; b < NB * 4; ++b)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) sum[b][j] = 0.f;
+        for (int d = t.depth;; d -= PART * BK) {
+          // (no call here: around one, not all of the sums could stay in registers)
+          if (lane == 0) ok = wait_inline(&tfull[hb & 1], (hb >> 1) & 1, abort_flag, g.err, g.wait_ns) ? 1 : 0;
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t ta = tmem_base + ((uint32_t)(quad * 32) << 16) + (hb & 1) * MAXN + cg * 32;
+#pragma unroll
+          for (int b = 0; b < NB * 4; ++b) {
+            if (cg * 32 + b / 4 * 64 >= t.cols) break;
+            const uint32_t at = ta + ((uint32_t)(b / 2 % 2 * 16) << 16) + b / 4 * 64 + b % 2 * 16;
+            float r[8];
+            tmem_ld16x16(at, r);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum[b][j] += r[j];
+            if (d <= PART * BK) tmem_st16x16(at, sum[b]);
+          }
+          if (d <= PART * BK) break;
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_read(free_bar[hb & 1]);
+          ++hb;
+        }
+        if (!ok) break;
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+      }
       for (int h = 0; h < t.halves; ++h) {
-        if (!zero) {
+        if (!zero && !parts) {
           if (lane == 0) ok = mbar_wait(&tfull[hb & 1], (hb >> 1) & 1, abort_flag, g.err, g.wait_ns) ? 1 : 0;
           ok = __shfl_sync(0xffffffffu, ok, 0);
           if (!ok) break;
@@ -745,25 +868,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
           __syncwarp();  // (the staging's last reads)
           if (MODE == GMM_DW) {
             uint32_t r[2][16];
+            float v[2][16];
             if (!zero) {
               tmem_ld16x32(tb + c, r[0]);
               tmem_ld16x32(tb + (16u << 16) + c, r[1]);
               tmem_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                v[0][j] = __uint_as_float(r[0][j]);
+                v[1][j] = __uint_as_float(r[1][j]);
+              }
             } else {
 #pragma unroll
-              for (int j = 0; j < 16; ++j) r[0][j] = r[1][j] = 0;
+              for (int j = 0; j < 16; ++j) v[0][j] = v[1][j] = 0.f;
             }
-            const int64_t o = ((int64_t)t.e * g.n + fw) * g.k + cb + c;
-            const int nr = NF - fw, nc = nv - c;
-            float* of = static_cast<float*>(g.out) + o;
-            __nv_bfloat16* ob = static_cast<__nv_bfloat16*>(g.out) + o;
-            if (g.out_f32) {
-              if (g.accumulate) store_dw<true>(r, of, g.k, nr, nc, lane);
-              else store_dw<false>(r, of, g.k, nr, nc, lane);
-            } else {
-              if (g.accumulate) store_dw<true>(r, ob, g.k, nr, nc, lane);
-              else store_dw<false>(r, ob, g.k, nr, nc, lane);
-            }
+            if (g.out_f32) put_dw<float>(g, v, t, fw, c, lane);
+            else put_dw<__nv_bfloat16>(g, v, t, fw, c, lane);
           } else {
             // lane = feature, 32 rows: through shared memory to 64-byte
             // pieces of the rows

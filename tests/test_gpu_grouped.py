@@ -394,3 +394,41 @@ def test_dw_of_more_rows_than_a_second_reads():
     v = x[rows].double()
     # (additions of zeros are exact)
     assert bool(((dw[0].double() - v.T @ v).abs() <= (len(rows) + 2) * 2.0 ** -23 * (v.abs().T @ v.abs())).all())
+
+
+@pytest.mark.parametrize("dw_dtype", [F32, BF])
+@pytest.mark.parametrize("n,k", [(72, 40), (200, 168), (264, 520)])
+def test_dw_of_parts(n, k, dw_dtype):
+    # reductions about the ends of the parts that are summed at once, and
+    # accumulating ones
+    p = Problem([767, 768, 769, 0, 832, 1536, 1537, 2305, 5], n, k, BF, lead=1, tail=2, seed=20)
+    out = p.run("dw", dw_dtype=dw_dtype)
+    p.check("dw", out)
+    base = torch.randn(out.shape, device="cuda", generator=torch.Generator("cuda").manual_seed(4)).to(dw_dtype)
+    acc = base.clone()
+    M.moe_grouped_matmul_dw(p.dy, p.x, p.offsets, acc, p.ws, accumulate=True)
+    p.check("dw", acc, base)
+
+
+@pytest.mark.parametrize("dw_dtype", [F32, BF])
+@pytest.mark.parametrize("n,k", [(72, 40), (264, 520)])
+def test_dw_of_many_rows_keeps_its_precision(n, k, dw_dtype):
+    # Positive rows, so that every error of a sum has one sign. Sums of 768 rows
+    # at most may be truncated, an addition by 2^-23 of itself (768 rows and 2 as
+    # above); the parts' sums are added up with a rounding of 2^-24 each
+    counts = [769, 1 << 20, 0, 4099]
+    p = Problem(counts, n, k, BF, lead=1, tail=1, seed=19)
+    for t in (p.x, p.dy):
+        t[1:-1] = t[1:-1].abs() + 0.5
+    out = p.run("dw", dw_dtype=dw_dtype)
+    base = torch.full_like(out, 1024.0)
+    acc = base.clone()
+    M.moe_grouped_matmul_dw(p.dy, p.x, p.offsets, acc, p.ws, accumulate=True)
+    for got, first in ((out, 0.0), (acc, 1024.0)):
+        for e, r in p.spans():
+            rows = r.stop - r.start
+            ref = p.dy[r].double().T @ p.x[r].double() + first
+            tol = (770 * 2.0 ** -23 + (rows // 768 + 2) * 2.0 ** -24) * ref
+            tol = tol + torch.finfo(dw_dtype).eps / 2 * (ref + tol)
+            assert bool(((got[e].double() - ref).abs() <= tol).all()), (e, ((got[e].double() - ref).abs() / ref).max())
+    assert M.moe_check_error(p.ws) == M.MOE_OK
