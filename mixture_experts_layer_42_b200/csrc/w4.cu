@@ -18,8 +18,10 @@ __device__ __forceinline__ float silu_f(float u) { return u / (1.0f + __expf(-u)
 
 // ---------------------------------------------------------------- quantizer
 
-// One warp per row i and 32 * CPT inputs: a lane holds 8 consecutive inputs,
-// group / 8 lanes a group.
+// One warp per row and 256 inputs: a lane holds 8 consecutive inputs, group / 8
+// lanes a group. 32 experts of 2048 x 7168: 780 us of bf16, 760 of fp32, 4.3
+// and 2.3 times what their bytes take; the loads by element and the 2-byte
+// stores of the scales, a row of outputs apart, are what is left.
 template <typename T>
 __global__ void __launch_bounds__(256) quantize_w4_kernel(const T* w, int64_t rows, int n, int k,
                                                           int group, uint8_t* q,
@@ -88,17 +90,21 @@ __global__ void __launch_bounds__(256) quantize_w4_kernel(const T* w, int64_t ro
 // g + 8 are the same feature of w1 and of w3, and a thread holds both sums.
 //
 // Measured: 128 tokens' down-projection (1024 rows, 256 experts of 7168 x
-// 2048, groups of 128) 417-423 us, 4.6 TB/s of codes, scales and rows; the
-// copies alone run at 6.4 TB/s, the arithmetic alone takes 393 us: issue slots
-// (28 of 72 million instructions turn codes into bf16, 20 move data). One
-// token's up-projection 36 us and down-projection 21 us: launch, the offsets
-// and a first round of loads, then 3.4 and 2.9 TB/s.
+// 2048, groups of 128) 417-423 us, 4.6 TB/s of codes, scales and rows, and 470
+// in a loop that the power cap slows; the copies alone run at 6.4 TB/s, the
+// arithmetic alone takes 393 us (28 of 72 million instructions turn codes into
+// bf16, 20 move data). Issue slots are 60 % full: three multiplying warps a
+// scheduler do not cover the way from a word's load through its conversion to
+// its MMA. One token's up-projection 36 us and down-projection 21 us: launch,
+// the offsets and a first round of loads, then 3.4 and 2.9 TB/s.
 //
 // The k order within 32 inputs (16 bytes of codes) is the codes' own: quad
 // lane t holds the word of inputs 8t..8t+7; (word >> 4s) & 0x000f000f are the
 // codes of inputs 8t+s and 8t+s+4, and or-ing 0x4300 makes them bf16 128 +
 // code (the mantissa's unit is 1 there), minus 136 the weight's integer, both
-// exact. The token rows' operand takes the same pairs.
+// exact: the conversion through a float's exponent and mantissa bits that Kim,
+// Henry, Fahim and Hassan Awadalla describe for fp16 ("Who Says Elephants Can't
+// Run", 2022). The token rows' operand takes the same pairs.
 
 using namespace tc;
 
@@ -552,8 +558,10 @@ cudaError_t launch_w4_group(const W4Args& g, const W4Tma& m, int64_t bound, int 
 
 template <bool SWIGLU>
 cudaError_t launch_w4_tokens(const W4Args& g, const W4Tma& m, int64_t bound, int num_sms, cudaStream_t st) {
-  // Token rows per tile, by the rows an expert has on average: more rows share
-  // their weights' way to operands, fewer leave less padding and more stages.
+  // Token rows per tile, by the rows an expert has on average, experts without
+  // rows counted (the host does not know the counts) and the shared MLP's rows
+  // not: more rows share their weights' way to operands, fewer leave less
+  // padding and more stages. Measured at one shape:
   // Down-projection of 256 experts of 7168 x 2048 with 8 / 16 / 32, uniform
   // routing: 417 / 440 / 451 us at 4 rows, 450 / 464 / 477 at 5, 493 / 485 /
   // 496 at 6, 700 / 573 / 577 at 10, 811 / 659 / 620 at 12. Skewed routing
