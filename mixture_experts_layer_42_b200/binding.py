@@ -509,17 +509,13 @@ def _check_w4_layer(c: moe_config, x, w_router, bias, w4, y, weights_out, idx_ou
     _need(x.dim() == 2 and x.shape[1] == D and x.dtype == dt, f"x must be {dt} [T, {D}]")
     T = x.shape[0]
 
-    def is_(t, name, shape, dtype):
-        _need(t.shape == shape and t.dtype == dtype, f"{name} must be {dtype} {list(shape)}")
-
-    is_(w_router, "w_router", (E, D), dt)
-    is_(y, "y", (T, D), dt)
+    _need(w_router.numel() == E * D and w_router.dtype == dt, f"w_router must be {dt} [{E}, {D}]")
     if c.has_bias and bias is not None:
-        is_(bias, "bias", (E,), torch.float32)
-    if weights_out is not None:
-        is_(weights_out, "weights_out", (T, c.topk), torch.float32)
-    if idx_out is not None:
-        is_(idx_out, "idx_out", (T, c.topk), torch.int32)
+        _need(bias.numel() == E and bias.dtype == torch.float32, f"bias must be float32 [{E}]")
+    # the outputs may be larger buffers
+    for t, name, rows, dtype in ((y, "y", D, dt), (weights_out, "weights_out", c.topk, torch.float32),
+                                 (idx_out, "idx_out", c.topk, torch.int32)):
+        _need(t is None or (t.numel() >= T * rows and t.dtype == dtype), f"{name} must be {dtype} [{T}, {rows}]")
     if w4.shapes is None:
         return
     want = dict(w1=(E, I, D), w3=(E, I, D), w2=(E, D, I), ws1=(1, Is, D), ws3=(1, Is, D), ws2=(1, D, Is))

@@ -255,7 +255,8 @@ def test_w4_layer_tensors_are_checked_against_the_configuration(M):
     refused("bias must be", b=z(4))
     refused("y must be", y=z(7, 128))
     refused("y must be", y=z(8, 128, dtype=F))
-    refused("weights_out must be", wo=z(8, 4, dtype=F))
+    refused("weights_out must be", wo=z(8, 2))
+    refused("weights_out must be", wo=z(7, 2, dtype=F))
     refused("idx_out must be", io=z(8, 2, dtype=torch.int64))
     for name, shape in (("w1", (4, 64, 64)), ("w3", (3, 64, 128)), ("w2", (4, 64, 128)), ("ws1", (1, 128, 128)),
                         ("ws2", None)):
