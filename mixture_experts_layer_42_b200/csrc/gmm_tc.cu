@@ -34,8 +34,8 @@
 // What bounds it, and what it measured (V3 sizes, 256 experts of 2048 x 7168,
 // cold; the memory's copy rate is 6.5 TB/s): 1024 rows read at 7.2 TB/s (1022
 // us); 65536 rows 1700-1840 us and skewed 2120-2340 us, dw of 24576 rows of 64
-// experts of 1408 x 2048 156-167 us and of 16384 rows of 32 of 2048 x 7168 in
-// fp32 541-570 us, each at 10-11 TB/s between L2 and the SMs, dw's stores
+// experts of 1408 x 2048 149-165 us and of 16384 rows of 32 of 2048 x 7168 in
+// fp32 530-580 us, each at 10-11 TB/s between L2 and the SMs, dw's stores
 // counted, and 0.85-1.15 PFLOP/s. A loop of seconds is bound by the 1 kW power
 // cap (65536 rows: 2050-2250 us at 1.1-1.2 GHz). dw tiles of 256 x 512, whose
 // write-out nothing overlaps for want of a second accumulator, took 233 and
